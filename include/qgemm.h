@@ -73,8 +73,13 @@ typedef enum qg_dtype {
   QG_E4M3 = 3, /* OCP 8-bit float E4M3 ("fn": no infinities, max 448) */
   QG_I8 = 4,
   QG_I32 = 5,
-  QG_U4 = 6    /* unsigned 4-bit, packed 8 per uint32: element k = 8w + i in
+  QG_U4 = 6,   /* unsigned 4-bit, packed 8 per uint32: element k = 8w + i in
                   bits [4i, 4i+4) of word w of its row; ld counts words */
+  QG_E2M1 = 7, /* OCP 4-bit float E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+                  negatives), two codes per byte: element k of a row is in the
+                  low (k even) or high (k odd) half of byte k / 2; ld counts
+                  elements */
+  QG_E8M0 = 8  /* OCP 8-bit scale E8M0: byte e stands for 2^(e - 127), 255 for NaN */
 } qg_dtype;
 
 typedef enum qg_order { QG_ROW_MAJOR = 0, QG_COL_MAJOR = 1 } qg_order;
@@ -85,7 +90,8 @@ typedef enum qg_order { QG_ROW_MAJOR = 0, QG_COL_MAJOR = 1 } qg_order;
  *                U (fp8 A scales): ceil(M/group_mn) x ceil(K/group_k) fp32,
  *                U (int4 zero points): N x K/group_k int8 (values 0..15),
  *                V (int4 scales): N x ceil(K/group_k) fp16,
- *                V (fp8 B scales): ceil(N/group_mn) x ceil(K/group_k) fp32.
+ *                V (fp8 B scales): ceil(N/group_mn) x ceil(K/group_k) fp32,
+ *                U, V (MXFP4 scales): M (N) x ceil(K/32) QG_E8M0.
  *                For a grouped problem rows of A/C/D/U is the total row count
  *                and B/V give ONE group's shape.
  *   ld           leading dimension (elements; uint32 words for QG_U4).
@@ -158,7 +164,9 @@ typedef enum qg_quant_kind {
   QG_QUANT_INT4_ZP = 1,   /* B only: b = (q - zero_point) * V[n, k / group_k], V fp16;
                              with U given (asymmetric), zero_point = U[n, k / group_k],
                              U QG_I8 bytes (N x K/group_k, ld a multiple of 16) */
-  QG_QUANT_BLOCK_F32 = 2  /* e4m3 A or B: value = code * scale of its (group_mn x group_k) block */
+  QG_QUANT_BLOCK_F32 = 2, /* e4m3 A or B: value = code * scale of its (group_mn x group_k) block */
+  QG_QUANT_MX = 3         /* e2m1 A and B (MXFP4): value = code * 2^(scale - 127), one E8M0 scale
+                             per row and 32 elements of K (group_k 32, group_mn 1) */
 } qg_quant_kind;
 
 typedef struct qg_quant {
@@ -224,6 +232,10 @@ size_t qg_partials_size(void);
  *     U is M x >=1, V is N x >=1, any ld >= 1, 4-byte aligned) -> the exact
  *     int32 sum times U[m] * V[n] in fp32, then the float epilogue; D f32 |
  *     bf16 | fp16 (or int8 codes), C f32 | bf16 | fp16; not grouped/batched
+ *   A, B e2m1 + U, V e8m0 (MXFP4: QG_QUANT_MX on both, group_k 32, group_mn
+ *     1) -> D f32 | bf16 | fp16, C f32 | bf16 | fp16. A block whose scale is
+ *     255 (NaN) makes the outputs that read it NaN. Codes past K, scales past
+ *     ceil(K/32) and a row's other padding are never used, whatever they hold.
  *   float paths with QG_EPI_QUANT_I8 -> D int8
  *   any of these grouped over experts (Adesc.num = Bdesc.num = E, offsets),
  *   and all but int4 batched (num = batch count on every operand, no offsets).
@@ -237,6 +249,40 @@ int qg_run(qg_handle* h, const qg_operation* op, float alpha,
            const void* C, const qg_layout* Cdesc,
            void* D, const qg_layout* Ddesc,
            const qg_workspace* ws, hipStream_t stream);
+
+/* ---- MXFP4 operands ------------------------------------------------------ */
+typedef enum qg_mx_act {
+  QG_MX_IDENTITY = 0, /* y[i, k] = x[i, k] */
+  QG_MX_SWIGLU = 1    /* y[i, k] = silu(x[i, k]) * x[i, K + k], silu(g) = g / (1 + exp(-g)) */
+} qg_mx_act;
+
+/* Quantises y = act(X), rows x K, to MXFP4 along K. A block of 32 elements
+ * (the last one of a row may be shorter) with largest magnitude amax takes the
+ * scale 2^(floor(log2 amax) - 2), at least 2^-127 (byte 0, which an all-zero
+ * block gets too); an element becomes the E2M1 value nearest to it over the
+ * scale, ties to the even code, magnitudes past 6 becoming 6. A block that
+ * holds a NaN or an infinity gets the scale 255 and zero codes. The codes are those
+ * of y without any rounding before them, the SwiGLU's too.
+ *   X     f32 | bf16 | fp16, T x K (IDENTITY) or T x 2K (SWIGLU, gate columns
+ *         first; K need not keep the second half aligned).
+ *   rows  NULL (then T = rows of Q), or a DEVICE int32 array with one entry
+ *         per row of Q: row i of Q comes from row rows[i] of X (a router's
+ *         gather). An entry outside [0, T) gives a row of zeros.
+ *   Q     QG_E2M1, rows x K; S QG_E8M0, rows x ceil(K/32): the operand and
+ *         scale operand of qg_run as they are (of a grouped run too). Codes
+ *         past K in the last block are written as zero; other padding is
+ *         left alone.
+ * The layouts are those of qg_run's operands: a grouped one (offsets) counts
+ * as its whole rows, a batched one is refused. Every pointer and row pitch
+ * must be a multiple of 16 bytes (`rows`: 4 bytes). Asynchronous on `stream`,
+ * allocates nothing. */
+int qg_mx_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc, const int32_t* rows, void* Q,
+                   const qg_layout* Qdesc, void* S, const qg_layout* Sdesc, hipStream_t stream);
+/* Y[i, k] = value of code Q[i, k] times its block's scale, rounded once (RNE)
+ * to Y's type (f32 | bf16 | fp16); NaN where the scale is 255. Same layouts
+ * and rules. */
+int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const void* S, const qg_layout* Sdesc, void* Y,
+                     const qg_layout* Ydesc, hipStream_t stream);
 
 /* qg_run without a workspace argument, for callers that cannot allocate
  * device memory (code under HIP graph capture, tight serving loops, harnesses

@@ -17,23 +17,26 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqgemm.so")
 
 # ---- enums (include/qgemm.h) -------------------------------------------------
-F32, F16, BF16, E4M3, I8, I32, U4 = 0, 1, 2, 3, 4, 5, 6
+F32, F16, BF16, E4M3, I8, I32, U4, E2M1, E8M0 = 0, 1, 2, 3, 4, 5, 6, 7, 8
 ROW_MAJOR, COL_MAJOR = 0, 1
 POLICY_DEFAULT, POLICY_MEASURE, POLICY_REUSE, POLICY_FORCE = 0, 1, 2, 3
 EPI_ALPHA_BETA, EPI_BIAS, EPI_RELU, EPI_GELU, EPI_QUANT_I8 = 0, 1, 2, 4, 8
-QUANT_NONE, QUANT_INT4_ZP, QUANT_BLOCK_F32 = 0, 1, 2
+QUANT_NONE, QUANT_INT4_ZP, QUANT_BLOCK_F32, QUANT_MX = 0, 1, 2, 3
+MX_IDENTITY, MX_SWIGLU = 0, 1
 SCHED_AUTO, SCHED_DP, SCHED_SPLITK, SCHED_STREAMK = 0, 1, 2, 3
 
 OK = 0
 ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE = -1, -2, -3, -4
 ERR_NO_KERNEL, ERR_HIP, ERR_FORMAT, ERR_BUFFER_SMALL = -5, -6, -7, -8
 
-DTYPE_CODES = {"f32": F32, "f16": F16, "bf16": BF16, "e4m3": E4M3, "i8": I8, "i32": I32, "u4": U4}
+DTYPE_CODES = {"f32": F32, "f16": F16, "bf16": BF16, "e4m3": E4M3, "i8": I8, "i32": I32, "u4": U4,
+               "e2m1": E2M1, "e8m0": E8M0}
 
 EXPORTS = ["qg_create", "qg_destroy", "qg_barriers_size", "qg_partials_size", "qg_run", "qg_plan",
            "qg_export", "qg_import", "qg_get_tuning_seq", "qg_cache_size", "qg_kernel_count",
            "qg_kernel_name", "qg_status_str", "qg_version", "qg_streamk_units", "qg_streamk_fixup",
-           "qg_run_noalloc", "qg_noalloc_barriers_size", "qg_noalloc_partials_size", "qg_run_timed"]
+           "qg_run_noalloc", "qg_noalloc_barriers_size", "qg_noalloc_partials_size", "qg_run_timed",
+           "qg_mx_quantize", "qg_mx_dequantize"]
 
 
 class Layout(ctypes.Structure):
@@ -91,6 +94,8 @@ def _load(path=LIB_PATH):
     L.qg_run_timed.argtypes = [vp, P(Operation), ctypes.c_float, vp, P(Layout), vp, P(Layout), vp, P(Layout), vp,
                                P(Layout), ctypes.c_float, vp, P(Layout), vp, P(Layout), P(Workspace), vp,
                                vp, ctypes.c_int64, P(ctypes.c_int64)]
+    L.qg_mx_quantize.argtypes = [vp, i32, vp, P(Layout), vp, vp, P(Layout), vp, P(Layout), vp]
+    L.qg_mx_dequantize.argtypes = [vp, vp, P(Layout), vp, P(Layout), vp, P(Layout), vp]
     L.qg_noalloc_barriers_size.restype = sz
     L.qg_noalloc_partials_size.restype = sz
     L.qg_plan.argtypes = [vp, P(Operation), P(Layout), P(Layout), P(Layout), P(Layout), P(Layout), P(Layout),
@@ -109,7 +114,8 @@ def _load(path=LIB_PATH):
     L.qg_streamk_fixup.argtypes = [i32, i32, i32, i32, P(ctypes.c_int32), i32, P(i32)]
     for name in ("qg_create", "qg_destroy", "qg_run", "qg_run_noalloc", "qg_run_timed", "qg_plan", "qg_export",
                  "qg_import",
-                 "qg_get_tuning_seq", "qg_cache_size", "qg_streamk_units", "qg_streamk_fixup"):
+                 "qg_get_tuning_seq", "qg_cache_size", "qg_streamk_units", "qg_streamk_fixup",
+                 "qg_mx_quantize", "qg_mx_dequantize"):
         getattr(L, name).restype = i32
     return L
 
@@ -167,9 +173,11 @@ def streamk_fixup(tiles, iters, programs, tile):
 
 
 def layout(dtype, rows, cols, ld=None, num=0, offsets=0, stride=0, order=ROW_MAJOR) -> Layout:
+    """ld defaults to the shortest pitch: cols (U4: words), or cols rounded up to
+    16 bytes for the MXFP4 operands, 32 codes (E2M1) or 16 scales (E8M0)."""
     t = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
     if ld is None:
-        ld = cols // 8 if t == U4 else cols
+        ld = cols // 8 if t == U4 else -(-cols // 32) * 32 if t == E2M1 else -(-cols // 16) * 16 if t == E8M0 else cols
     return Layout(t, order, int(rows), int(cols), int(ld), int(num), 0, int(offsets or 0), int(stride))
 
 
@@ -246,6 +254,29 @@ class Gemm:
                               stream if stream is not None else _current_stream(), _ptr(stamps), int(units_cap),
                               ctypes.byref(n))
         return st, n.value
+
+    def mx_quantize_raw(self, X, Xd, Q, Qd, S, Sd, act=MX_IDENTITY, rows=None, stream=None) -> int:
+        """qg_mx_quantize; returns the status code."""
+        def r(x):
+            return None if x is None else ctypes.byref(x)
+        return lib.qg_mx_quantize(self.h, int(act), _ptr(X), r(Xd), _ptr(rows), _ptr(Q), r(Qd), _ptr(S), r(Sd),
+                                  stream if stream is not None else _current_stream())
+
+    def mx_quantize(self, *args, **kw):
+        """Rows of X (all, or those that the device int32 array `rows` names) to
+        MXFP4 codes Q and scales S, through `act` (MX_IDENTITY, MX_SWIGLU)."""
+        _check(self.mx_quantize_raw(*args, **kw), "qg_mx_quantize")
+
+    def mx_dequantize_raw(self, Q, Qd, S, Sd, Y, Yd, stream=None) -> int:
+        """qg_mx_dequantize; returns the status code."""
+        def r(x):
+            return None if x is None else ctypes.byref(x)
+        return lib.qg_mx_dequantize(self.h, _ptr(Q), r(Qd), _ptr(S), r(Sd), _ptr(Y), r(Yd),
+                                    stream if stream is not None else _current_stream())
+
+    def mx_dequantize(self, *args, **kw):
+        """MXFP4 codes Q and scales S to the values they stand for."""
+        _check(self.mx_dequantize_raw(*args, **kw), "qg_mx_dequantize")
 
     def plan(self, op, Ad, Ud, Bd, Vd, Cd, Dd, alpha, beta, ws=None) -> str:
         buf = ctypes.create_string_buffer(512)

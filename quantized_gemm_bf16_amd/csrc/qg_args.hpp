@@ -8,7 +8,7 @@ enum Mode : int32_t { MODE_DP = 0, MODE_SPLITK = 1, MODE_STREAMK = 2, MODE_GROUP
 
 enum EpiFlag : int32_t { EPI_BIAS = 1, EPI_RELU = 2, EPI_GELU = 4, EPI_QUANT_I8 = 8 };
 
-enum DType : int32_t { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_E4M3 = 3, DT_I8 = 4, DT_I32 = 5, DT_U4 = 6 };
+enum DType : int32_t { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_E4M3 = 3, DT_I8 = 4, DT_I32 = 5, DT_U4 = 6, DT_E2M1 = 7, DT_E8M0 = 8 };
 
 struct Args {
   // operands (device pointers)

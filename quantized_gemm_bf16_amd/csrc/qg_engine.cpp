@@ -23,6 +23,7 @@
 
 #include "../../include/qgemm.h"
 #include "qg_args.hpp"
+#include "qg_mx_quant.hpp"
 #include "qg_registry.hpp"
 #include "qg_streamk.hpp"
 
@@ -44,13 +45,16 @@ int esize(int t) {
     case DT_F16:
     case DT_BF16: return 2;
     case DT_E4M3:
-    case DT_I8: return 1;
+    case DT_I8:
+    case DT_E8M0: return 1;
     default: return 0;
   }
 }
+// Bytes of `n` elements of a row (E2M1: two to a byte, n even wherever it matters)
+int64_t row_bytes(int t, int64_t n) { return t == DT_E2M1 ? n / 2 : n * esize(t); }
 const char* dt_name(int t) {
-  static const char* n[] = {"f32", "f16", "bf16", "e4m3", "i8", "i32", "u4"};
-  return (t >= 0 && t <= 6) ? n[t] : "-";
+  static const char* n[] = {"f32", "f16", "bf16", "e4m3", "i8", "i32", "u4", "e2m1", "e8m0"};
+  return (t >= 0 && t <= 8) ? n[t] : "-";
 }
 const char* sched_name(int m) {
   switch (m) {
@@ -163,7 +167,7 @@ std::string cache_key(int64_t M, const std::string& pk) { return std::to_string(
 int check_layout(const qg_layout* L, bool need_rows_cols_ok = true) {
   if (!L) return QG_ERR_INVALID_ARG;
   if (L->order != QG_ROW_MAJOR) return L->order == QG_COL_MAJOR ? QG_ERR_UNSUPPORTED : QG_ERR_INVALID_ARG;
-  if (L->type < 0 || L->type > QG_U4) return QG_ERR_INVALID_ARG;
+  if (L->type < 0 || L->type > QG_E8M0) return QG_ERR_INVALID_ARG;
   if (need_rows_cols_ok && (L->rows < 0 || L->cols < 0)) return QG_ERR_INVALID_ARG;
   if (L->ld < 0) return QG_ERR_INVALID_ARG;
   // the kernels index rows, columns and pitches in 32 bits; bounding them
@@ -315,6 +319,33 @@ int validate(const qg_operation* op, float alpha, const void* A, const qg_layout
     p.ldu = Ud->ld;
     p.ldv = Vd->ld;
     if (!(p.td == QG_F32 || p.td == QG_BF16 || p.td == QG_F16 || p.td == QG_I8)) return QG_ERR_UNSUPPORTED;
+  } else if (p.ta == QG_E2M1) {
+    // MXFP4: one E8M0 scale per row and 32 elements of K on both operands
+    if (p.tb != QG_E2M1 || p.qa != QG_QUANT_MX || p.qb != QG_QUANT_MX) return QG_ERR_UNSUPPORTED;
+    if (op->quant_a.group_k != 32 || op->quant_b.group_k != 32 || op->quant_a.group_mn != 1 ||
+        op->quant_b.group_mn != 1)
+      return QG_ERR_UNSUPPORTED;
+    if (!Ud || !Vd) return QG_ERR_INVALID_ARG;
+    if ((st = check_layout(Ud)) || (st = check_layout(Vd))) return st;
+    if (Ud->type != QG_E8M0 || Vd->type != QG_E8M0) return QG_ERR_UNSUPPORTED;
+    const int64_t nb = cdiv(p.K, 32);
+    if (Ud->rows != p.M || Ud->cols != nb || Ud->ld < nb) return QG_ERR_INVALID_ARG;
+    if (Vd->rows != p.N || Vd->cols != nb || Vd->ld < nb) return QG_ERR_INVALID_ARG;
+    if (p.M > 0 && p.N > 0 && p.K > 0 && (!U || !V)) return QG_ERR_INVALID_ARG;
+    if (Ud->ld % 16 || Vd->ld % 16 || !aligned16(U) || !aligned16(V)) return QG_ERR_ALIGNMENT;
+    if (grouped) {
+      if (Vd->num != Ad->num) return QG_ERR_INVALID_ARG;
+      if (Ud->offsets && Ud->offsets != Ad->offsets) return QG_ERR_UNSUPPORTED;
+      p.v_batch = Vd->stride;
+      if (p.v_batch != 0 && p.v_batch < Vd->rows * Vd->ld) return QG_ERR_INVALID_ARG;
+      if (p.v_batch % 16 || Bd->stride % 32) return QG_ERR_ALIGNMENT;
+      if (!Ad->offsets && Ud->stride != Ud->rows * Ud->ld) return QG_ERR_UNSUPPORTED;
+    }
+    p.U = U;
+    p.V = V;
+    p.ldu = Ud->ld;
+    p.ldv = Vd->ld;
+    if (!(p.td == QG_F32 || p.td == QG_BF16 || p.td == QG_F16 || p.td == QG_I8)) return QG_ERR_UNSUPPORTED;
   } else {
     return QG_ERR_UNSUPPORTED;
   }
@@ -334,7 +365,8 @@ int validate(const qg_operation* op, float alpha, const void* A, const qg_layout
   const int64_t b_row_elems = p.tb == QG_U4 ? p.ldb * 8 : p.ldb;  // U4: ld counts words
   if (p.lda < p.K || b_row_elems < p.K || p.ldd < p.N) return QG_ERR_INVALID_ARG;
   if (p.tb == QG_U4 && p.K % 8) return QG_ERR_ALIGNMENT;
-  if ((p.lda * esize(p.ta)) % 16 || (p.ldb * esize(p.tb)) % 16 || (p.ldd * esize(p.td)) % 16) return QG_ERR_ALIGNMENT;
+  if (p.ta == QG_E2M1 && (p.lda % 32 || p.ldb % 32)) return QG_ERR_ALIGNMENT;  // 32 codes: 16 bytes
+  if (row_bytes(p.ta, p.lda) % 16 || row_bytes(p.tb, p.ldb) % 16 || row_bytes(p.td, p.ldd) % 16) return QG_ERR_ALIGNMENT;
   // K itself need not keep rows 16-byte aligned: the kernels read a row's
   // last partial 16-byte chunk whole (it lies inside the row pitch) and zero
   // its bytes past K on chip
@@ -365,8 +397,41 @@ int validate(const qg_operation* op, float alpha, const void* A, const qg_layout
   (void)V;
   (void)Vd;
   // 32-bit buffer offsets: a tile's rows must span less than 2 GiB
-  if (p.lda * esize(p.ta) * 256 >= (int64_t(1) << 31) || p.ldb * esize(p.tb) * 256 >= (int64_t(1) << 31))
+  if (row_bytes(p.ta, p.lda) * 256 >= (int64_t(1) << 31) || row_bytes(p.tb, p.ldb) * 256 >= (int64_t(1) << 31))
     return QG_ERR_UNSUPPORTED;
+  if (p.ta == QG_E2M1 && (p.ldu * 256 >= (int64_t(1) << 31) || p.ldv * 256 >= (int64_t(1) << 31))) return QG_ERR_UNSUPPORTED;
+  return QG_OK;
+}
+
+// ---- MXFP4 quantise / dequantise ----------------------------------------------
+// One operand of qg_mx_quantize / qg_mx_dequantize: rows x cols of `type`, at
+// a pitch of whole 16 bytes.
+int check_mx_operand(const void* ptr, const qg_layout* L, int64_t rows, int64_t cols) {
+  if (L->rows != rows || L->cols != cols || L->ld < cols) return QG_ERR_INVALID_ARG;
+  if (L->num > 1 && !L->offsets) return QG_ERR_UNSUPPORTED;  // batched
+  if (rows > 0 && cols > 0 && !ptr) return QG_ERR_INVALID_ARG;
+  if ((L->type == QG_E2M1 && L->ld % 32) || row_bytes(L->type, L->ld) % 16 || !aligned16(ptr)) return QG_ERR_ALIGNMENT;
+  return QG_OK;
+}
+
+// Shared checks of both directions; X / Y is `Vd` (values), rows x cols of it.
+int mx_args(const void* vals, const qg_layout* Vd, int64_t vrows, int64_t vcols, const void* Q, const qg_layout* Qd,
+            const void* S, const qg_layout* Sd, MxQuantArgs& a) {
+  int st;
+  if ((st = check_layout(Vd)) || (st = check_layout(Qd)) || (st = check_layout(Sd))) return st;
+  if (!(Vd->type == QG_F32 || Vd->type == QG_BF16 || Vd->type == QG_F16)) return QG_ERR_UNSUPPORTED;
+  if (Qd->type != QG_E2M1 || Sd->type != QG_E8M0) return QG_ERR_UNSUPPORTED;
+  if ((st = check_mx_operand(Q, Qd, Qd->rows, Qd->cols))) return st;
+  if ((st = check_mx_operand(S, Sd, Qd->rows, cdiv(Qd->cols, 32)))) return st;
+  if ((st = check_mx_operand(vals, Vd, vrows, vcols))) return st;
+  a.K = (int32_t)Qd->cols;
+  a.ldq = Qd->ld / 2;
+  a.lds = Sd->ld;
+  a.ldx = Vd->ld;
+  a.T = (int32_t)vrows;
+  a.x_type = Vd->type;
+  a.Q = (char*)const_cast<void*>(Q);
+  a.S = (char*)const_cast<void*>(S);
   return QG_OK;
 }
 
@@ -374,6 +439,7 @@ int validate(const qg_operation* op, float alpha, const void* A, const qg_layout
 bool compatible(const KernelInfo& k, const Problem& p) {
   if (k.family == FAM_W4) return p.ta == QG_BF16 && p.tb == QG_U4 && p.E == 0;
   if (k.family == FAM_F8) return p.ta == QG_E4M3 && p.tb == QG_E4M3;
+  if (k.family == FAM_MX) return p.ta == QG_E2M1 && p.tb == QG_E2M1;
   if (k.family != FAM_TILE && k.family != FAM_SKINNY) return false;
   if (k.family == FAM_SKINNY && p.M > k.bm && p.E == 0) return false;  // skinny tiles cover all rows
   return k.in_type == p.ta && p.tb == p.ta;
@@ -538,6 +604,11 @@ Choice heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, i
                  int forced_split = 0) {
   Choice c;
   const int cus = h->cus;
+  if (p.E > 0 && p.ta == QG_E2M1) {
+    c.kernel = kernel_by_shape(p, 128, 128);
+    c.mode = MODE_GROUPED;
+    return c;
+  }
   if (p.E > 0 && p.ta == QG_E4M3) {
     c.kernel = kernel_by_shape(p, p.batched && p.M <= 64 ? 64 : 128, 256);
     c.mode = MODE_GROUPED;
@@ -580,6 +651,8 @@ Choice heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, i
   }
   if (p.ta == QG_E4M3) {
     c.kernel = kernel_by_shape(p, p.M <= 64 ? 64 : 128, 256);
+  } else if (p.ta == QG_E2M1) {
+    c.kernel = kernel_by_shape(p, 128, 128);
   } else if (p.M <= 32) {
     // Skinny GEMM: aim for about one workgroup per compute unit.
     int64_t target = cdiv(p.N, cus);
@@ -925,6 +998,42 @@ int qg_run_timed(qg_handle* h, const qg_operation* op, float alpha, const void* 
   pl.a.stamps = stamps;
   if (!h->online) return QG_ERR_HIP;
   return launch(pl, stream);
+}
+
+int qg_mx_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc, const int32_t* rows, void* Q,
+                   const qg_layout* Qdesc, void* S, const qg_layout* Sdesc, hipStream_t stream) {
+  if (!h || !Xdesc || !Qdesc || !Sdesc) return QG_ERR_INVALID_ARG;
+  if (act != QG_MX_IDENTITY && act != QG_MX_SWIGLU) return QG_ERR_INVALID_ARG;
+  MxQuantArgs a{};
+  const int64_t vrows = rows ? Xdesc->rows : Qdesc->rows;
+  const int64_t vcols = act == QG_MX_SWIGLU ? 2 * Qdesc->cols : Qdesc->cols;
+  const int st = mx_args(X, Xdesc, vrows, vcols, Q, Qdesc, S, Sdesc, a);
+  if (st != QG_OK) return st;
+  if (reinterpret_cast<uintptr_t>(rows) & 3) return QG_ERR_ALIGNMENT;
+  if (Qdesc->rows == 0 || Qdesc->cols == 0) return QG_OK;
+  a.X = X;
+  a.rows = rows;
+  a.swiglu = act == QG_MX_SWIGLU;
+  a.cpr = (int32_t)(cdiv(Qdesc->cols, 32) * 4);
+  a.units = Qdesc->rows * a.cpr;
+  if (mx_quant_blocks(a.units) > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (!h->online) return QG_ERR_HIP;
+  return launch_mx_quantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+
+int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const void* S, const qg_layout* Sdesc, void* Y,
+                     const qg_layout* Ydesc, hipStream_t stream) {
+  if (!h || !Ydesc || !Qdesc || !Sdesc) return QG_ERR_INVALID_ARG;
+  MxQuantArgs a{};
+  const int st = mx_args(Y, Ydesc, Qdesc->rows, Qdesc->cols, Q, Qdesc, S, Sdesc, a);
+  if (st != QG_OK) return st;
+  if (Qdesc->rows == 0 || Qdesc->cols == 0) return QG_OK;
+  a.Y = Y;
+  a.cpr = (int32_t)cdiv(Qdesc->cols, 8);
+  a.units = Qdesc->rows * a.cpr;
+  if (mx_quant_blocks(a.units) > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (!h->online) return QG_ERR_HIP;
+  return launch_mx_dequantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_plan(qg_handle* h, const qg_operation* op, const qg_layout* Adesc, const qg_layout* Udesc,

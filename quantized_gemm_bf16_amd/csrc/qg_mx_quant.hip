@@ -1,0 +1,313 @@
+// MXFP4 quantise and dequantise kernels.
+//
+// A block of 32 values along K shares the scale 2^(floor(log2 amax) - 2) (E8M0
+// byte: amax's exponent field less 2); a value over the scale is rounded to
+// the nearest E2M1 value (0, 0.5, 1, 1.5, 2, 3, 4, 6), ties to even, past 6 to
+// 6. Scaling by a power of two is exact, so a code is one rounding of the
+// value, done by v_cvt_scalef32_pk_fp4_f32.
+//
+// Both kernels are bound by memory: an element costs its own 2 or 4 bytes
+// and 17/32 byte of MXFP4. One lane takes a unit of 8 consecutive elements
+// (one 16-byte access of 16-bit values, one dword of codes), the four lanes
+// of a quad take one block, so the block maximum is two DPP exchanges and
+// nothing goes through LDS. Units are numbered row after row, whatever K is, so
+// that a wave is full at any width; a workgroup does one division to find its
+// first row and its lanes one multiplication each.
+//
+// SwiGLU: the codes are those of silu(g) * u without rounding before them, so
+// fp32 arithmetic alone would put values next to a rounding border on its
+// wrong side (about one in 10^6). The fp32 value v is within 2^-18 of the
+// exact one (for g >= -32: the argument of exp2 is off by at most 48 * 2^-24,
+// the other steps by a few 2^-23). Each lane rounds v (1 - 2^-17) and v (1 + 2^-17)
+// instead of v: equal codes are the exact value's code. Where they differ, or
+// the block maximum is as near a power of two, or fp32's range or the bound
+// does not hold, the wave redoes its units in 64 bits.
+#include "qg_mx_quant.hpp"
+
+#include "qg_args.hpp"
+#include "qg_device.hpp"
+
+namespace qg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+typedef i32x4 __attribute__((aligned(2))) i32x4_u2;
+
+// Rounds two values (already over their scale) to E2M1 codes in byte SEL of a dword.
+template <int SEL>
+__device__ __forceinline__ uint32_t cvt_fp4(uint32_t old, float a, float b) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, 1.0f, SEL);
+}
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float m) {
+  uint32_t q = 0;
+  q = cvt_fp4<0>(q, v[0] * m, v[1] * m);
+  q = cvt_fp4<1>(q, v[2] * m, v[3] * m);
+  q = cvt_fp4<2>(q, v[4] * m, v[5] * m);
+  q = cvt_fp4<3>(q, v[6] * m, v[7] * m);
+  return q;
+}
+
+// Maximum over the four lanes of a quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+  return x;
+}
+
+// Eight elements as loaded: one 16-byte chunk of 16-bit values or two of fp32.
+template <int DT>
+struct Raw {
+  static constexpr int ES = DT == DT_F32 ? 4 : 2;
+  i32x4 d[DT == DT_F32 ? 2 : 1];
+  // n of the eight exist (the rest read as zero); p is aligned to 16 bytes
+  // where AL, else to the element
+  template <bool AL>
+  __device__ __forceinline__ void load(const char* p, int n) {
+    if (n >= 8) {
+#pragma unroll
+      for (int i = 0; i < ES / 2; ++i) d[i] = AL ? ((const i32x4*)p)[i] : ((const i32x4_u2*)p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < ES / 2; ++i) d[i] = i32x4{};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) {
+          if constexpr (ES == 4)
+            d[j / 4][j % 4] = ((const int*)p)[j];
+          else
+            d[0][j / 2] |= (int)((uint32_t)((const uint16_t*)p)[j] << (16 * (j & 1)));
+        }
+    }
+  }
+  __device__ __forceinline__ float at(int j) const {
+    // (a copy: a bit cast of a vector's element itself would take element 0)
+    const uint32_t w = (uint32_t)(DT == DT_F32 ? d[j / 4][j % 4] : d[0][j / 2]);
+    if constexpr (DT == DT_F32) return __builtin_bit_cast(float, w);
+    if constexpr (DT == DT_BF16) return __builtin_bit_cast(float, j & 1 ? w & 0xFFFF0000u : w << 16);
+    return f16_bits_to_f32((uint16_t)(j & 1 ? w >> 16 : w));
+  }
+};
+
+// Row and unit-in-row of unit `first + off` (off < 2^16): `first` is
+// workgroup-uniform, so its division is done once.
+struct Place {
+  int64_t row;
+  int unit;
+};
+struct Places {
+  int64_t row0;
+  uint32_t u0, cpr, magic;
+  __device__ __forceinline__ Places(int64_t first, int cpr_) : cpr((uint32_t)cpr_) {
+    row0 = first < (int64_t(1) << 32) ? (int64_t)((uint32_t)first / cpr) : first / cpr_;
+    u0 = (uint32_t)(first - row0 * cpr_);
+    // n / cpr = (n * magic) >> 32 is exact for n * cpr < 2^32; a workgroup
+    // crosses at most one row's end where rows have 2^15 units or more
+    magic = cpr > 1 ? 0xFFFFFFFFu / cpr + 1 : 0;
+  }
+  __device__ __forceinline__ Place at(uint32_t off) const {
+    uint32_t n = u0 + off, q;
+    if (cpr >= (1u << 15)) {
+      q = n >= cpr;
+    } else {
+      q = cpr == 1 ? n : __umulhi(n, magic);
+    }
+    return Place{row0 + q, (int)(n - q * cpr)};
+  }
+};
+
+// Codes (low half) and scale byte (high half) of eight values silu(g) u, in 64
+// bits. Called by whole waves: the block's maximum is taken over the quad.
+template <int DT>
+__device__ __attribute__((noinline)) uint64_t swiglu_codes64(Raw<DT> g, Raw<DT> u) {
+  double v[8], top = 0;
+  int bad = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double x = g.at(j);
+    v[j] = x / (1.0 + exp(-x)) * (double)u.at(j);
+    const double m = fabs(v[j]);
+    bad |= !(m <= 1.7976931348623157e308);
+    top = m > top ? m : top;
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    const double o = __shfl_xor(top, d, 64);
+    top = o > top ? o : top;
+    bad |= __shfl_xor(bad, d, 64);
+  }
+  if (bad) return (uint64_t)255 << 32;
+  const int e = (int)((__builtin_bit_cast(uint64_t, top) >> 52) & 0x7FF) - 1023 - 2 + 127;
+  const int byte = max(0, min(254, e));
+  const double inv = __builtin_bit_cast(double, (uint64_t)(127 - byte + 1023) << 52);
+  uint32_t q = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double t = fabs(v[j]) * inv;
+    // even codes take the ties: <= below them, < above
+    const uint32_t c = (t > 0.25) + (t >= 0.75) + (t > 1.25) + (t >= 1.75) + (t > 2.5) + (t >= 3.5) + (t > 5.0);
+    q |= (c | (v[j] < 0 ? 8u : 0u)) << (4 * j);
+  }
+  return q | (uint64_t)byte << 32;
+}
+
+template <int DT, bool GATED, int U>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const MxQuantArgs a) {
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * U);
+  const Places places(first, a.cpr);
+  Raw<DT> x[U], up[GATED ? U : 1];
+  Place at[U];
+  bool live[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t off = i * kThreads + threadIdx.x;
+    live[i] = first + off < a.units;  // the same for a whole quad: units come in fours
+    at[i] = places.at(off);
+    int64_t src = at[i].row;
+    if (a.rows && live[i]) src = a.rows[at[i].row];
+    const int k = at[i].unit * 8;
+    const int n = live[i] && src >= 0 && src < a.T ? a.K - k : 0;
+    const char* p = (const char*)a.X + (src * a.ldx + k) * Raw<DT>::ES;
+    x[i].template load<true>(p, n);
+    if constexpr (GATED) up[i].template load<false>(p + (int64_t)a.K * Raw<DT>::ES, n);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    float v[8];
+    uint32_t top = 0, q;
+    int byte;
+    bool redo = false;
+    float low = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = x[i].at(j);
+      if constexpr (GATED) {
+        low = fminf(low, v[j]);
+        const float e = __builtin_amdgcn_exp2f(v[j] * -1.44269504f);
+        v[j] = v[j] * __builtin_amdgcn_rcpf(1.f + e) * up[i].at(j);
+      }
+      top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
+    }
+    top = quad_max(top);
+    byte = max((int)(top >> 23) - 2, 0);
+    const float inv = __builtin_bit_cast(float, (uint32_t)(254 - min(byte, 252)) << 23);
+    if constexpr (GATED) {
+      constexpr float kOff = 0x1p-17f;
+      q = codes8(v, inv * (1.f - kOff));
+      const float t = __builtin_bit_cast(float, top);
+      redo = codes8(v, inv * (1.f + kOff)) != q || top >= 0x7F000000u || (top != 0 && t < 0x1p-60f) || low < -32.f ||
+             (__builtin_bit_cast(uint32_t, t * (1.f - kOff)) ^ __builtin_bit_cast(uint32_t, t * (1.f + kOff))) >> 23;
+      if (__any(redo)) {
+        const uint64_t r = swiglu_codes64<DT>(x[i], up[i]);
+        q = (uint32_t)r;
+        byte = (int)(r >> 32);
+      }
+    } else {
+      q = codes8(v, inv);
+      if (top >= 0x7F800000u) q = 0, byte = 255;
+    }
+    if (live[i]) {
+      *(uint32_t*)(a.Q + at[i].row * a.ldq + at[i].unit * 4) = q;
+      if ((threadIdx.x & 3) == 0) a.S[at[i].row * a.lds + (at[i].unit >> 2)] = (char)byte;
+    }
+  }
+}
+
+template <int DT, int U>
+__global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantArgs a) {
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * U);
+  const Places places(first, a.cpr);
+  uint32_t q[U], s[U];
+  Place at[U];
+  bool live[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const uint32_t off = i * kThreads + threadIdx.x;
+    live[i] = first + off < a.units;
+    at[i] = places.at(off);
+    q[i] = s[i] = 0;
+    if (live[i]) {
+      q[i] = *(const uint32_t*)(a.Q + at[i].row * a.ldq + at[i].unit * 4);
+      s[i] = (uint8_t)a.S[at[i].row * a.lds + (at[i].unit >> 2)];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (!live[i]) continue;
+    // 2^(s - 127): byte 0 is fp32's subnormal 2^-127, byte 255 NaN
+    const float scale = __builtin_bit_cast(float, s[i] == 255 ? 0x7FC00000u : s[i] ? s[i] << 23 : 0x00400000u);
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      const uint32_t b = q[i] >> (8 * h);
+      const f32x2 y = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(b, 1.0f, 0);
+      v[2 * h] = y[0] * scale;
+      v[2 * h + 1] = y[1] * scale;
+    }
+    const int k = at[i].unit * 8;
+    const int64_t base = at[i].row * a.ldx + k;
+    if constexpr (DT == DT_F32) {
+      float* y = (float*)a.Y + base;
+      if (k + 8 <= a.K) {
+        ((f32x4*)y)[0] = f32x4{v[0], v[1], v[2], v[3]};
+        ((f32x4*)y)[1] = f32x4{v[4], v[5], v[6], v[7]};
+      } else {
+        for (int j = 0; j < 8; ++j)
+          if (k + j < a.K) y[j] = v[j];
+      }
+    } else {
+      uint16_t* y = (uint16_t*)a.Y + base;
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = DT == DT_BF16 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
+      if (k + 8 <= a.K) {
+        *(i32x4*)y = i32x4{(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16),
+                           (int)(h[6] | h[7] << 16)};
+      } else {
+        for (int j = 0; j < 8; ++j)
+          if (k + j < a.K) y[j] = (uint16_t)h[j];
+      }
+    }
+  }
+}
+
+template <int DT, bool GATED>
+hipError_t quantize_u(const MxQuantArgs& a, int cus, hipStream_t s) {
+  hipLaunchKernelGGL((mx_quantize_kernel<DT, GATED, 1>), dim3((unsigned)mx_quant_blocks(a.units)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+template <int DT>
+hipError_t quantize_g(const MxQuantArgs& a, int cus, hipStream_t s) {
+  return a.swiglu ? quantize_u<DT, true>(a, cus, s) : quantize_u<DT, false>(a, cus, s);
+}
+template <int DT>
+hipError_t dequantize_u(const MxQuantArgs& a, int cus, hipStream_t s) {
+  hipLaunchKernelGGL((mx_dequantize_kernel<DT, 1>), dim3((unsigned)mx_quant_blocks(a.units)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t mx_quant_blocks(int64_t units) { return (units + kThreads - 1) / kThreads; }
+
+hipError_t launch_mx_quantize(const MxQuantArgs& a, int cus, hipStream_t s) {
+  switch (a.x_type) {
+    case DT_F32: return quantize_g<DT_F32>(a, cus, s);
+    case DT_F16: return quantize_g<DT_F16>(a, cus, s);
+    case DT_BF16: return quantize_g<DT_BF16>(a, cus, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, int cus, hipStream_t s) {
+  switch (a.x_type) {
+    case DT_F32: return dequantize_u<DT_F32>(a, cus, s);
+    case DT_F16: return dequantize_u<DT_F16>(a, cus, s);
+    case DT_BF16: return dequantize_u<DT_BF16>(a, cus, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace qg

@@ -3,6 +3,7 @@
 #include "qg_registry.hpp"
 #include "qg_w4.hpp"
 #include "qg_fp8.hpp"
+#include "qg_mx.hpp"
 
 namespace qg {
 
@@ -21,7 +22,10 @@ namespace qg {
   extern template hipError_t launch_w4<W4Cfg<MT, BN, WN, WK, ST>>(const Args&, int, hipStream_t);
 #define QG_F8(BM, BN, WM, WN, ST) \
   extern template hipError_t launch_f8<F8Cfg<BM, BN, WM, WN, ST>>(const Args&, int, hipStream_t);
+#define QG_MX(BM, BN, WM, WN, ST, RB) \
+  extern template hipError_t launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>(const Args&, int, hipStream_t);
 #include "qg_kernel_list.inc"
+#undef QG_MX
 #undef QG_W4
 #undef QG_F8
 #undef QG_TILE_BF16
@@ -56,6 +60,11 @@ namespace qg {
 #define QG_F8(BM, BN, WM, WN, ST)                                                                         \
   {"f8_E4M3_" #BM "x" #BN "_w" #WM "x" #WN "_s" #ST, FAM_F8, DT_E4M3, BM, BN, 128, ST, WM * WN * 64, BM * BN * 4, \
    &launch_f8<F8Cfg<BM, BN, WM, WN, ST>>},
+
+#define QG_MX(BM, BN, WM, WN, ST, RB)                                                                      \
+  {"mx_" #BM "x" #BN "x" #RB "b_w" #WM "x" #WN "_s" #ST, FAM_MX, DT_E2M1, BM, BN,                          \
+   MxCfg<BM, BN, WM, WN, ST, RB>::BK, ST, MxCfg<BM, BN, WM, WN, ST, RB>::NT, BM * BN * 4,                  \
+   &launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>},
 
 // (not const: a const table would also be placed in device constant memory)
 KernelInfo kKernels[] = {
