@@ -440,6 +440,7 @@ bool compatible(const KernelInfo& k, const Problem& p) {
   if (k.family == FAM_W4) return p.ta == QG_BF16 && p.tb == QG_U4 && p.E == 0;
   if (k.family == FAM_F8) return p.ta == QG_E4M3 && p.tb == QG_E4M3;
   if (k.family == FAM_MX) return p.ta == QG_E2M1 && p.tb == QG_E2M1;
+  if (k.family == FAM_MX_SKINNY) return p.ta == QG_E2M1 && p.tb == QG_E2M1 && (p.M <= k.bm || p.E > 0);
   if (k.family != FAM_TILE && k.family != FAM_SKINNY) return false;
   if (k.family == FAM_SKINNY && p.M > k.bm && p.E == 0) return false;  // skinny tiles cover all rows
   return k.in_type == p.ta && p.tb == p.ta;
@@ -598,17 +599,71 @@ int skinny_for(const Problem& p, int64_t target_bn) {
   return best;
 }
 
+// MXFP4. Few rows stream B: up to 16 rows of a plain product take the
+// k-interleaved skinny kernel (1 x 4096 x 14336: 9.2 us, 64 x 64 tiles 13.4), up
+// to 32 its wider form while one workgroup per 16 columns fits on the CUs
+// (32 x 4096 x 14336: 11.8 against 13.4; N = 8192: 20 against 16.8), experts with
+// up to 4 rows on average the one that shares A (64 experts, 128 rows, N 2048,
+// K 7168: 85 us, 64 x 64 tiles 88, 128 x 128 tiles 98). Otherwise the square tile
+// with the least estimated time: a CU that has n tiles takes n (fixed + step per
+// 256 of K), step being less for a tile that has the CU to itself and no
+// neighbour to share the L2 with. Measured, us, tiles of 64 / 128 / 256:
+//   128 x 4096 x 4096       8.9 /  14 /   -      512 x 8192 x 8192        36 /  25 /   -
+//   4096 x 4096 x 4096       73 /  53 /  48      64 experts, 1024 rows    98 / 102 /   -
+//   64 experts, 4096 rows   137 / 130 / 148      16384 rows              336 / 250 / 237
+//   8 experts, 16384 rows, N 4096, K 1000        139 / 119 /  86
+Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, int forced_mode) {
+  Choice c;
+  const double cus = h->cus;
+  const bool grouped = p.E > 0 && !p.batched;
+  c.mode = p.E > 0 ? MODE_GROUPED : MODE_DP;
+  const int64_t rows = grouped ? cdiv(p.M, p.E) : p.M;  // of one product
+  if (rows <= 4 && p.E > 0) {
+    c.kernel = kernel_by_shape(p, 16, 64);
+  } else if (!grouped && (rows <= 16 || (rows <= 32 && cdiv(p.N, 16) <= h->cus))) {
+    c.kernel = kernel_by_shape(p, rows <= 16 ? 16 : 32, 16);
+  }
+  if (c.kernel >= 0) return c;
+  static const struct {
+    int side;
+    double fixed, alone, step;
+  } kTiles[] = {{64, 1.1, 0.3, 0.25}, {128, 3.5, 0.65, 0.75}, {256, 7.5, 2.4, 2.4}};
+  const double steps = (double)cdiv(p.K, 256);
+  double best = 0;
+  for (const auto& t : kTiles) {
+    // m-tiles: exact, or with every expert that has rows ending inside a tile half the time
+    const double live = (double)std::min<int64_t>(p.E, p.M);
+    const double tm = grouped ? std::max(live, (double)cdiv(p.M, t.side) + live / 2)
+                              : (double)cdiv(p.M, t.side) * (p.batched ? p.E : 1);
+    const double n = std::max(1.0, std::ceil(tm * (double)cdiv(p.N, t.side) / cus));
+    const double us = n * (t.fixed + steps * (n > 1 ? t.step : t.alone));
+    if (c.kernel >= 0 && us >= best) continue;
+    const int k = kernel_by_shape(p, t.side, t.side);
+    if (k >= 0) c.kernel = k, best = us;
+  }
+  // A long K over few tiles: up to eight chunks that fit on the CUs together,
+  // four k-tiles each at least, where they save more than the 5 us that the
+  // partial tiles cost (64 x 1024 x 14336: 11.1 us in eight chunks, 20 whole,
+  // 13.5 in fourteen).
+  if (c.kernel < 0 || p.E > 0 || forced_mode >= 0 || !ws || !ws->partials || !ws->barriers) return c;
+  const KernelInfo& k = kKernels[c.kernel];
+  const int64_t tiles = cdiv(p.M, k.bm) * cdiv(p.N, k.bn), iters = cdiv(p.K, k.bk);
+  const int64_t s = std::min<int64_t>({8, h->cus / std::max<int64_t>(tiles, 1), iters / 4});
+  if (k.bm == 64 && s > 1 && 0.3 * (double)(iters - cdiv(iters, s)) > 5 &&
+      (size_t)tiles * s * k.slot_bytes <= ws->partials_size && (size_t)tiles * 4 <= ws->barriers_size) {
+    c.mode = MODE_SPLITK;
+    c.split = (int)s;
+  }
+  return c;
+}
+
 // Shape heuristic used on a cache miss. `mode` / `split` are the schedule the
 // caller forces (MODE_DP with split 0 = nothing forced).
 Choice heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, int forced_mode = -1,
                  int forced_split = 0) {
   Choice c;
   const int cus = h->cus;
-  if (p.E > 0 && p.ta == QG_E2M1) {
-    c.kernel = kernel_by_shape(p, 128, 128);
-    c.mode = MODE_GROUPED;
-    return c;
-  }
+  if (p.ta == QG_E2M1) return mx_heuristic(h, p, ws, forced_mode);
   if (p.E > 0 && p.ta == QG_E4M3) {
     c.kernel = kernel_by_shape(p, p.batched && p.M <= 64 ? 64 : 128, 256);
     c.mode = MODE_GROUPED;
@@ -651,8 +706,6 @@ Choice heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, i
   }
   if (p.ta == QG_E4M3) {
     c.kernel = kernel_by_shape(p, p.M <= 64 ? 64 : 128, 256);
-  } else if (p.ta == QG_E2M1) {
-    c.kernel = kernel_by_shape(p, 128, 128);
   } else if (p.M <= 32) {
     // Skinny GEMM: aim for about one workgroup per compute unit.
     int64_t target = cdiv(p.N, cus);

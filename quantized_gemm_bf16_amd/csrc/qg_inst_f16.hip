@@ -18,5 +18,6 @@ namespace qg {
 #define QG_W4(MT, BN, WN, WK, ST)
 #define QG_F8(BM, BN, WM, WN, ST)
 #define QG_MX(BM, BN, WM, WN, ST, RB)
+#define QG_MX_SKINNY(BN, NW, MT, DP, SH)
 #include "qg_kernel_list.inc"
 }  // namespace qg

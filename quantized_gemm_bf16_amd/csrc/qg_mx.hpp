@@ -65,27 +65,57 @@ __device__ __forceinline__ void lds_dword_trim(char* p, int keep) {
   asm volatile("" ::: "memory");
 }
 
+// Byte address in LDS of a shared array, for load_lds_x4s. Taken once: each
+// conversion of a generic pointer costs a 64-bit add, a compare and a select.
+__device__ __forceinline__ uint32_t lds_address(void* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)p);
+}
+// As load_lds_x4 (qg_device.hpp), to an LDS address and with a scalar offset.
+// The hardware checks voff against the resource's size less soff, which must
+// not exceed that size.
+__device__ __forceinline__ void load_lds_x4s(const i32x4& rsrc, uint32_t lds_wave_base, uint32_t voff, uint32_t soff) {
+  const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds_wave_base);
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(m0v), "v"(voff), "s"(rsrc), "s"(soff)
+      : "memory", "m0");
+}
+// A copy of a lane's value that the compiler cannot move out of the branch it
+// is taken in (as pinned(), for values that differ between lanes).
+__device__ __forceinline__ int pinned_lane(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // ---- tiles ------------------------------------------------------------------
-// The LDS ring, swizzle, load issue and epilogue of the tile core, with
-// ROWB bytes (2 ROWB codes) of each row and their ROWB / 16 scales per stage.
-// The scales follow the operand tiles in a stage as planes of one dword per row
-// (A's rows, then B's): plane h holds the dword of lane half h, or, where a
-// k-tile has only 4 scales (64 bytes of codes), one plane serves both halves.
+// The LDS ring, swizzle and epilogue of the tile core, with ROWB bytes (2 ROWB
+// codes) of each row per stage. What bounds the loop is less the 32 cycles of
+// an instruction than feeding it: a stage's loads pass the CU's address unit
+// at 64 bytes a cycle, and a wave that issues them in a row stands still as
+// long. So
+//  - every wave issues its own loads one by one between its MFMAs, for the
+//    k-tile STAGES - 1 ahead, whose stage the last barrier freed;
+//  - scales have a ring of their own, SPANS spans of 16 bytes (512 codes) per
+//    row, A's rows and then B's, two of them loaded together: what the L2 can
+//    serve is a number of requests, and a k-tile's 4 or 8 bytes of scales of a
+//    row would cost it as much as the row's 64 or 128 bytes of codes.
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int ROWB_>
 struct MxCfg : TileCfg<El::E4M3, BM_, BN_, WM_, WN_, STAGES_, ROWB_> {
   using Base = TileCfg<El::E4M3, BM_, BN_, WM_, WN_, STAGES_, ROWB_>;
-  static constexpr int BK = 2 * ROWB_;          // codes per k-tile
-  static constexpr int KS = ROWB_ / 32;         // MFMAs along k per k-tile
-  static constexpr int PLANES = ROWB_ / 64;     // scale dwords per row and k-tile
-  static constexpr int HALF = Base::NW / 2;     // waves that issue the loads
-  static constexpr int SL = PLANES * (BM_ + BN_) / 64;  // 64-lane scale loads per stage
-  static constexpr int LSA = PLANES * BM_ / 64 / HALF, LSB = PLANES * BN_ / 64 / HALF;  // ... of one issuing wave
-  static constexpr int LS = LSA + LSB;
-  static constexpr int STAGE = Base::STAGE_BYTES + SL * 256;
-  static constexpr int LPH = 2 * Base::LPW + LS;        // loads of an issuing wave per stage
-  static_assert(LS * HALF == SL && BM_ % 64 == 0 && BN_ % 64 == 0, "scale rows must split evenly over the issuing waves");
-  static_assert(STAGES_ * STAGE <= 160 * 1024 - 1024, "LDS budget");
-  static_assert(LPH * (STAGES_ - 1) < 64, "vmcnt range");
+  static constexpr int BK = 2 * ROWB_;           // codes per k-tile
+  static constexpr int KS = ROWB_ / 32;          // MFMAs along k per k-tile
+  static constexpr int KPS = 256 / ROWB_;        // k-tiles per span of scales
+  static constexpr int GA = BM_ / 64, GT = (BM_ + BN_) / 64;  // 64-row scale loads per span: of A, in all
+  static constexpr int SPAN = (BM_ + BN_) * 16;
+  static constexpr int RING = STAGES_ * Base::STAGE_BYTES;
+  static_assert(BM_ % 64 == 0 && BN_ % 64 == 0 && GT <= Base::NW, "a wave loads the scales of 64 rows");
+  // Spans in the ring, and how many before their own two are loaded: a wave's
+  // loads are known to have landed STAGES - 2 k-tiles after the one that they went out in.
+  static constexpr int SPANS = KPS >= STAGES_ - 1 ? 3 : 4, LEAD = SPANS - 2;
+  static_assert(STAGES_ >= 2 && LEAD * KPS >= STAGES_ - 1, "scales land in the k-tiles between their load and their use");
+  static_assert(RING + SPANS * SPAN <= 160 * 1024 - 4352, "LDS budget");
 };
 
 template <class Cfg>
@@ -93,118 +123,93 @@ struct Mx : Tile<Cfg> {
   using Base = Tile<Cfg>;
   using Acc = typename Base::Acc;
   static constexpr int TM = Cfg::TM, TN = Cfg::TN, BM = Cfg::BM, BN = Cfg::BN, NT = Cfg::NT;
-  static constexpr int SMEM_BYTES = Cfg::STAGES * Cfg::STAGE;
+  static constexpr int SMEM_BYTES = Cfg::RING + Cfg::SPANS * Cfg::SPAN;
 
   __device__ __forceinline__ static void mainloop(const Args& a, const Unit& u, char* smem, Acc& acc) {
     const int w = wave_id(), l = lane_id();
     const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
     const int64_t lda_b = a.lda / 2, ldb_b = a.ldb / 2;
-    const uint32_t K = (uint32_t)a.K, nb = (K + 31) / 32;
+    const uint32_t K = (uint32_t)a.K;
     const int a_rows = max(0, min(BM, u.m_end - u.m0));
     const int b_rows = max(0, min(BN, a.N - u.n0));
     const i32x4 rA = make_rsrc_words((const char*)a.A + (int64_t)u.m0 * lda_b, (uint32_t)(a_rows * lda_b));
     const i32x4 rB = make_rsrc_words((const char*)a.B + (int64_t)u.expert * (a.b_batch / 2) + (int64_t)u.n0 * ldb_b,
                                      (uint32_t)(b_rows * ldb_b));
-    const i32x4 rU = make_rsrc_words((const char*)a.U + (int64_t)u.m0 * a.ldu, (uint32_t)(a_rows * a.ldu));
-    const i32x4 rV = make_rsrc_words((const char*)a.V + (int64_t)u.expert * a.v_batch + (int64_t)u.n0 * a.ldv,
-                                     (uint32_t)(b_rows * a.ldv));
+    // this wave's scales: 64 rows of A or of B (where there are fewer such
+    // groups than waves, some waves repeat one: the same bytes to the same place)
+    const int grp = w % Cfg::GT;
+    const bool of_a = grp < Cfg::GA;
+    const int64_t ld_s = of_a ? a.ldu : a.ldv;
+    const i32x4 rS = make_rsrc_words(of_a ? (const char*)a.U + (int64_t)u.m0 * a.ldu
+                                          : (const char*)a.V + (int64_t)u.expert * a.v_batch + (int64_t)u.n0 * a.ldv,
+                                     (uint32_t)((of_a ? a_rows : b_rows) * ld_s));
+    const uint32_t offS = (uint32_t)(((of_a ? grp : grp - Cfg::GA) * 64 + l) * ld_s);
 
-    // As in the tile core: the first half of the waves issues every load of a
-    // stage, wave w filling its own row slots and those of wave w + HALF.
-    constexpr int CPR = Cfg::CPR, RPI = Cfg::RPI, ROWB = Cfg::ROWB, HALF = Cfg::HALF, LA = Cfg::LA, LB = Cfg::LB;
-    static_assert((HALF * LA * RPI) % 16 == 0 && (HALF * LB * RPI) % 16 == 0,
-                  "the second half's rows keep the swizzle key (period 16 rows)");
-    uint32_t offA[LA], offB[LB], chA[LA], chB[LB];
+    constexpr int CPR = Cfg::CPR, RPI = Cfg::RPI, ROWB = Cfg::ROWB, LA = Cfg::LA, LPW = Cfg::LPW, KPS = Cfg::KPS;
+    // Load i < LA of a wave fills RPI rows of A's part of a stage, the others of
+    // B's: lane l -> row l / CPR, physical chunk l % CPR, whose logical chunk
+    // begins at byte chunk(i, l) of the row's k-tile.
+    auto row_of = [&](int i, int ll) { return (i < LA ? w * LA + i : w * Cfg::LB + i - LA) * RPI + ll / CPR; };
+    auto chunk = [&](int i, int ll) { return (uint32_t)(((ll % CPR) ^ swz<CPR>(row_of(i, ll))) * 16); };
+    uint32_t off[LPW];
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      const int row = (w * LA + i) * RPI + l / CPR;
-      chA[i] = (uint32_t)(((l % CPR) ^ swz<CPR>(row)) * 16);
-      offA[i] = (uint32_t)(row * lda_b) + chA[i];
-    }
-#pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      const int row = (w * LB + i) * RPI + l / CPR;
-      chB[i] = (uint32_t)(((l % CPR) ^ swz<CPR>(row)) * 16);
-      offB[i] = (uint32_t)(row * ldb_b) + chB[i];
-    }
-    const uint32_t stepA = (uint32_t)(HALF * LA * RPI * lda_b), stepB = (uint32_t)(HALF * LB * RPI * ldb_b);
-    // A wave's scale load i: of A for i < LSA, else of B; 64 rows of a plane.
-    constexpr int LSA = Cfg::LSA, LS = Cfg::LS, GA = BM / 64, GB = BN / 64;
-    uint32_t offS[LS], plS[LS], ldsS[LS];  // row offset, plane, place in the stage
-#pragma unroll
-    for (int i = 0; i < LS; ++i) {
-      const int j = i < LSA ? w * LSA + i : w * Cfg::LSB + i - LSA;
-      const int g = i < LSA ? j % GA : j % GB;
-      plS[i] = (uint32_t)(i < LSA ? j / GA : j / GB);
-      offS[i] = (uint32_t)((g * 64 + l) * (i < LSA ? a.ldu : a.ldv));
-      ldsS[i] = Cfg::STAGE_BYTES + (plS[i] * (BM + BN) + (i < LSA ? 0 : BM) + g * 64) * 4;
-    }
+    for (int i = 0; i < LPW; ++i) off[i] = (uint32_t)(row_of(i, l) * (i < LA ? lda_b : ldb_b)) + chunk(i, l);
+    char* spans = smem + Cfg::RING;
+    const uint32_t lds = lds_address(smem);
+    const uint32_t dstA = lds + w * LA * 1024, dstB = lds + Cfg::A_BYTES + w * Cfg::LB * 1024;
+    const uint32_t dstS = lds + Cfg::RING + grp * 1024;
 
-    auto issue = [&](int stage, int kt) {
-      if (w >= HALF) return;
-      char* sbase = smem + stage * Cfg::STAGE;
+    // Load i of k-tile kt into ring stage `stage`. FULL: the k-tile lies wholly
+    // before K; otherwise chunks past K read as zero (lane: the lane's number).
+    auto load = [&](auto FULL, int i, int stage, int kt, int lane) {
       const uint32_t kk = (uint32_t)kt * ROWB;
-      const bool live = kt < u.ke;
+      const bool in = decltype(FULL)::value || 2 * (kk + chunk(i, lane)) < K;
+      const uint32_t dst = (i < LA ? dstA + i * 1024 : dstB + (i - LA) * 1024) + stage * Cfg::STAGE_BYTES;
+      load_lds_x4s(i < LA ? rA : rB, dst, in ? off[i] : kOOB, kk);
+    };
+    // Scales of spans [j, end); those past K do not exist.
+    const int spans_k = (int)((K + 511) / 512);
+    auto load_spans = [&](int j, int end) {
+      for (; j < min(end, spans_k); ++j) load_lds_x4s(rS, dstS + j % Cfg::SPANS * Cfg::SPAN, offS, (uint32_t)j * 16);
+    };
+    // Spans 2 i and 2 i + 1 are loaded at the first k-tile of span 2 i - LEAD:
+    // every wave has read the scales of all spans before that one by then, and
+    // the two that they replace, SPANS before them, are such.
+    constexpr int LEAD = Cfg::LEAD;
+    auto load_next_spans = [&](int kt) {
+      if (kt % (2 * KPS) == LEAD % 2 * KPS && kt != u.kb) load_spans(kt / KPS + LEAD, kt / KPS + LEAD + 2);
+    };
+    auto load_tile = [&](int stage, int kt) {
+      const int ll = pinned_lane(l);  // keeps this rare work out of the loops' registers
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ws = w + h * HALF;
-        if (live && 2 * (kk + ROWB) <= K) {
-#pragma unroll
-          for (int i = 0; i < LA; ++i) load_lds_x4(rA, sbase + (ws * LA + i) * 1024, offA[i] + h * stepA + kk);
-#pragma unroll
-          for (int i = 0; i < LB; ++i)
-            load_lds_x4(rB, sbase + Cfg::A_BYTES + (ws * LB + i) * 1024, offB[i] + h * stepB + kk);
-        } else {
-#pragma unroll
-          for (int i = 0; i < LA; ++i)
-            load_lds_x4(rA, sbase + (ws * LA + i) * 1024,
-                        live && 2 * (kk + chA[i]) < K ? offA[i] + h * stepA + kk : kOOB);
-#pragma unroll
-          for (int i = 0; i < LB; ++i)
-            load_lds_x4(rB, sbase + Cfg::A_BYTES + (ws * LB + i) * 1024,
-                        live && 2 * (kk + chB[i]) < K ? offB[i] + h * stepB + kk : kOOB);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        const uint32_t block = (uint32_t)kt * CPR + plS[i] * 4;
-        load_lds_x1a(i < LSA ? rU : rV, sbase + ldsS[i], live && block < nb ? offS[i] + block : kOOB);
-      }
+      for (int i = 0; i < LPW; ++i) load(std::false_type{}, i, stage, kt, ll);
     };
 
-    // The k-tile that holds K's end, where that is not on whole scale dwords:
-    // the lane that loaded a chunk zeroes the codes past K in it, and the
-    // scales past the last block, before the barrier that publishes the stage.
-    const int ktail = (K & 127) ? (int)((K - 1) / (2 * ROWB)) : -1;
+    // Before the barrier that publishes them, the lanes that loaded them zero
+    // what lies past K: codes in the last chunk of a row (K not a multiple of
+    // 32), in the k-tile that holds it, and scales in the last span (their
+    // number not a multiple of 16: past it is the caller's padding, and a 255
+    // there is a NaN even beside zero codes), once its first k-tile is resident.
+    const int nb = (int)((K + 31) / 32);
+    const int tail_codes = (K & 31) ? (int)((K - 1) / (2 * ROWB)) : -1;
+    const int tail_scales = (nb & 15) ? max(u.kb, (nb - 1) / 16 * KPS) : -1;
     auto trim = [&](int stage, int kt) {
-      if (w >= HALF) return;
-      const uint32_t ke = pinned(K);  // keeps this work inside the branch
-      char* sbase = smem + stage * Cfg::STAGE;
-      const uint32_t kk = (uint32_t)kt * ROWB;
+      const int ll = pinned_lane(l);
+      const uint32_t ke = pinned(K);
+      if (kt == tail_codes) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ws = w + h * HALF;
-#pragma unroll
-        for (int i = 0; i < LA; ++i) {
-          const int keep = (int)(ke - 2 * (kk + chA[i]));
-          if (keep > 0 && keep < 32) lds_chunk_trim_codes(sbase + (ws * LA + i) * 1024 + l * 16, keep);
-        }
-#pragma unroll
-        for (int i = 0; i < LB; ++i) {
-          const int keep = (int)(ke - 2 * (kk + chB[i]));
-          if (keep > 0 && keep < 32) lds_chunk_trim_codes(sbase + Cfg::A_BYTES + (ws * LB + i) * 1024 + l * 16, keep);
+        for (int i = 0; i < LPW; ++i) {
+          const int keep = (int)(ke - 2 * ((uint32_t)kt * ROWB + chunk(i, ll)));
+          char* p = smem + stage * Cfg::STAGE_BYTES + (i < LA ? (w * LA + i) * 1024 : Cfg::A_BYTES + (w * Cfg::LB + i - LA) * 1024);
+          if (keep > 0 && keep < 32) lds_chunk_trim_codes(p + ll * 16, keep);
         }
       }
-#pragma unroll
-      for (int i = 0; i < LS; ++i) {
-        const int keep = (int)((ke + 31) / 32) - (kt * CPR + (int)plS[i] * 4);
-        if (keep > 0 && keep < 4) lds_dword_trim(sbase + ldsS[i] + l * 4, keep);
-      }
+      if (kt == tail_scales)
+        lds_chunk_trim(spans + kt / KPS % Cfg::SPANS * Cfg::SPAN + grp * 1024 + ll * 16, (int)((ke + 31) / 32) & 15);
     };
 
     // Fragments of k-step ks: lane l takes row l % 32 and chunk KS h + ks of
-    // its half h; the scales of all its chunks are one dword (PLANES 2) or
-    // the h-th half of one.
+    // its half h; the scales of its KS chunks are consecutive bytes.
     constexpr int KS = Cfg::KS;
     const int orow = l & 31, ohalf = l >> 5;
     struct Frags {
@@ -214,43 +219,35 @@ struct Mx : Tile<Cfg> {
       int a[TM], b[TN];
     };
     auto read_frags = [&](int stage, int ks, Frags& f) {
-      const char* sA = smem + stage * Cfg::STAGE;
+      const char* sA = smem + stage * Cfg::STAGE_BYTES;
       const char* sB = sA + Cfg::A_BYTES;
       const int c = ohalf * KS + ks;
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) {
-        const int row = wm * Cfg::WTM + tm * 32 + orow;
-        f.a[tm] = *(const i32x4*)(sA + row * ROWB + ((c ^ swz<CPR>(row)) << 4));
-      }
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) {
         const int row = wn * Cfg::WTN + tn * 32 + orow;
         f.b[tn] = *(const i32x4*)(sB + row * ROWB + ((c ^ swz<CPR>(row)) << 4));
       }
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) {
+        const int row = wm * Cfg::WTM + tm * 32 + orow;
+        f.a[tm] = *(const i32x4*)(sA + row * ROWB + ((c ^ swz<CPR>(row)) << 4));
+      }
     };
-    auto read_scales = [&](int stage, Scales& s) {
-      const int* p = (const int*)(smem + stage * Cfg::STAGE + Cfg::STAGE_BYTES);
-      if constexpr (Cfg::PLANES == 2) p += ohalf * (BM + BN);
+    auto read_scales = [&](int kt, Scales& s) {
+      // KS 4: the k-tile's 8 scales are a dword per half; KS 2: one dword, two bytes per half
+      const char* p = spans + kt / KPS % Cfg::SPANS * Cfg::SPAN + kt % KPS * (ROWB / 16) + (KS == 4 ? ohalf * 4 : 0);
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm) s.a[tm] = p[wm * Cfg::WTM + tm * 32 + orow];
+      for (int tm = 0; tm < TM; ++tm) s.a[tm] = *(const int*)(p + (wm * Cfg::WTM + tm * 32 + orow) * 16);
 #pragma unroll
-      for (int tn = 0; tn < TN; ++tn) s.b[tn] = p[BM + wn * Cfg::WTN + tn * 32 + orow];
-      if constexpr (Cfg::PLANES == 1) {
+      for (int tn = 0; tn < TN; ++tn) s.b[tn] = *(const int*)(p + (BM + wn * Cfg::WTN + tn * 32 + orow) * 16);
+    };
+    auto half_scales = [&](Scales& s) {
+      if constexpr (KS == 2) {
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) s.a[tm] = (int)((uint32_t)s.a[tm] >> (16 * ohalf));
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) s.b[tn] = (int)((uint32_t)s.b[tn] >> (16 * ohalf));
       }
-    };
-    // MFMAs of k-step KI over the n-tiles [tn0, tn1) of the wave tile.
-    auto mma = [&](auto KI, const Frags& f, const Scales& s, int tn0, int tn1) {
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
-          if (tn < tn0 || tn >= tn1) continue;
-          acc.v[tn][tm] = mfma_mx<decltype(KI)::value>(f.b[tn], f.a[tm], acc.v[tn][tm], s.b[tn], s.a[tm]);
-        }
     };
 
 #pragma unroll
@@ -258,47 +255,83 @@ struct Mx : Tile<Cfg> {
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm) acc.v[tn][tm] = f32x16{};
 
-    const int nk = u.ke - u.kb;
+    // The k-tiles before `fast` prefetch a whole k-tile and find nothing to
+    // trim in the next one; they wait for the next stage's loads only
+    // (counting codes: where scales were loaded since, for a load more). The
+    // last ones wait for all of what is left.
     constexpr int S = Cfg::STAGES;
+    const int whole = min(u.ke, (int)(K / (2 * ROWB)));  // k-tiles [kb, whole) are whole
+    int fast = whole - S + 1;
+    if (tail_scales >= 0) fast = min(fast, tail_scales - 1);
+    fast = max(fast, u.kb);
+    load_spans(u.kb / KPS, ((u.kb / KPS + LEAD) & ~1) + 2);  // all that no later k-tile of the unit loads
 #pragma unroll
-    for (int st = 0; st < S; ++st) issue(st, u.kb + st);
-    wait_vmcnt<Cfg::LPH*(S - 1)>();
-    if (u.kb == ktail) trim(0, ktail);
+    for (int st = 0; st < S - 1; ++st)
+      if (u.kb + st < u.ke) load_tile(st, u.kb + st);
+    if (u.kb + S - 1 <= u.ke)
+      wait_vmcnt<LPW*(S - 2)>();
+    else
+      wait_vmcnt<0>();
+    if (u.kb == tail_codes || u.kb == tail_scales) trim(0, u.kb);
     lds_barrier();
     Frags cur;
     Scales sc;
     read_frags(0, 0, cur);
-    read_scales(0, sc);
-    for (int it = 0; it < nk; ++it) {
-      const int st = it % S;
+    read_scales(u.kb, sc);
+    half_scales(sc);
+    int st = 0, ahead = S - 1;  // stages of k-tile kt and of the one being loaded
+    constexpr int NM = TM * TN, EARLY = NM / 2;  // MFMAs of a k-step; those of the last one before the barrier
+    auto step = [&](auto FAST, int kt) {
+      constexpr bool F = decltype(FAST)::value;
+      const int next = st + 1 == S ? 0 : st + 1;
+      load_next_spans(kt);
+      if constexpr (!F)
+        if (kt + S - 1 < u.ke) load_tile(ahead, kt + S - 1);
       static_for<KS>([&](auto KI) {
         constexpr int ks = decltype(KI)::value;
+        constexpr bool last = ks + 1 == KS;
         Frags nxt;
-        if constexpr (ks + 1 < KS) {
-          read_frags(st, ks + 1, nxt);
-          mma(KI, cur, sc, 0, TN);
-          interleave_reads<TM + TN, TM * TN>();
-        } else {
-          // Last k-step of this stage, as in the tile core: half of its MFMAs
-          // cover the wait for the next stage, the rest the next stage's
-          // first fragments and scales.
-          Scales ns;
-          mma(KI, cur, sc, 0, TN / 2);
-          wait_vmcnt<Cfg::LPH*(S - 2)>();
-          if (u.kb + it + 1 == ktail) trim((it + 1) % S, ktail);
-          lds_barrier();
-          issue(st, u.kb + it + S);
-          read_frags((it + 1) % S, 0, nxt);
-          read_scales((it + 1) % S, ns);
-          mma(KI, cur, sc, TN / 2, TN);
-          interleave_reads<2 * (TM + TN), TM*(TN - TN / 2)>();
+        Scales ns;
+        if constexpr (!last) read_frags(st, ks + 1, nxt);
+        // Loads [l0, l1) of the k-tile ahead go out in this k-step, in the last
+        // one before the barrier. With two stages that k-tile is the next one:
+        // its loads go out in the first half, the second half lets them land.
+        constexpr int LK = S == 2 ? KS / 2 : KS;
+        constexpr int l0 = ks < LK ? LPW * ks / LK : LPW, l1 = ks < LK ? LPW * (ks + 1) / LK : LPW, room = last ? EARLY : NM;
+        static_for<NM>([&](auto MI) {
+          constexpr int m = decltype(MI)::value, tn = m / TM, tm = m % TM;
+          if constexpr (F) {
+            static_for<l1 - l0>([&](auto LI) {
+              constexpr int j = decltype(LI)::value;
+              if constexpr (j * room / (l1 - l0) == m) {
+                load(std::true_type{}, l0 + j, ahead, kt + S - 1, l);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            });
+          }
+          if constexpr (last && m == EARLY) {
+            // the next stage has landed and every wave has read this one
+            wait_vmcnt<F ? LPW*(S - 2) : 0>();
+            if constexpr (!F)
+              if (kt + 1 == tail_codes || kt + 1 == tail_scales) trim(next, kt + 1);
+            lds_barrier();
+            read_frags(next, 0, nxt);
+            read_scales(kt + 1, ns);
+          }
+          acc.v[tn][tm] = mfma_mx<ks>(cur.b[tn], cur.a[tm], acc.v[tn][tm], sc.b[tn], sc.a[tm]);
+        });
+        if constexpr (last) {
+          half_scales(ns);
           sc = ns;
         }
         cur = nxt;
       });
-    }
-    // the ring still receives the zeros of k-tiles past the unit (see the tile core)
-    wait_vmcnt<0>();
+      ahead = st;
+      st = next;
+    };
+    int kt = u.kb;
+    for (; kt < fast; ++kt) step(std::true_type{}, kt);
+    for (; kt < u.ke; ++kt) step(std::false_type{}, kt);
     __syncthreads();
   }
 };

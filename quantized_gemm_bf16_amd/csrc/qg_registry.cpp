@@ -3,7 +3,7 @@
 #include "qg_registry.hpp"
 #include "qg_w4.hpp"
 #include "qg_fp8.hpp"
-#include "qg_mx.hpp"
+#include "qg_mx_skinny.hpp"
 
 namespace qg {
 
@@ -24,8 +24,11 @@ namespace qg {
   extern template hipError_t launch_f8<F8Cfg<BM, BN, WM, WN, ST>>(const Args&, int, hipStream_t);
 #define QG_MX(BM, BN, WM, WN, ST, RB) \
   extern template hipError_t launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>(const Args&, int, hipStream_t);
+#define QG_MX_SKINNY(BN, NW, MT, DP, SH) \
+  extern template hipError_t launch_mx_skinny<MxSkinnyCfg<BN, NW, MT, DP, SH>>(const Args&, int, hipStream_t);
 #include "qg_kernel_list.inc"
 #undef QG_MX
+#undef QG_MX_SKINNY
 #undef QG_W4
 #undef QG_F8
 #undef QG_TILE_BF16
@@ -65,6 +68,10 @@ namespace qg {
   {"mx_" #BM "x" #BN "x" #RB "b_w" #WM "x" #WN "_s" #ST, FAM_MX, DT_E2M1, BM, BN,                          \
    MxCfg<BM, BN, WM, WN, ST, RB>::BK, ST, MxCfg<BM, BN, WM, WN, ST, RB>::NT, BM * BN * 4,                  \
    &launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>},
+
+#define QG_MX_SKINNY(BN, NW, MT, DP, SH)                                                                       \
+  {"mx_skinny_" #MT "x16x" #BN "_w" #NW "_d" #DP "_" #SH, FAM_MX_SKINNY, DT_E2M1, 16 * MT, BN,                  \
+   MxSkinnyCfg<BN, NW, MT, DP, SH>::BK, DP, NW * 64, 16 * MT * BN * 4, &launch_mx_skinny<MxSkinnyCfg<BN, NW, MT, DP, SH>>},
 
 // (not const: a const table would also be placed in device constant memory)
 KernelInfo kKernels[] = {

@@ -184,7 +184,7 @@ def test_product_every_kernel_and_schedule_plans(g):
     d = operands(16, 512, 4096)
     for i, name in enumerate(qg.kernel_names()):
         for s in (qg.SCHED_DP, qg.SCHED_SPLITK, qg.SCHED_STREAMK):
-            op = qg.operation(policy=qg.POLICY_FORCE, schedule=s, split_k=2, kernel=i, quant_a=MX, quant_b=MX)
+            op = qg.operation(policy=qg.POLICY_FORCE, schedule=s, split_k=2, programs=8, kernel=i, quant_a=MX, quant_b=MX)
             if name.startswith("mx"):
                 assert f"kernel={name} " in plan(g, d, op, ws)
             else:
