@@ -1069,7 +1069,7 @@ int qg_mx_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc,
   a.swiglu = act == QG_MX_SWIGLU;
   a.cpr = (int32_t)(cdiv(Qdesc->cols, 32) * 4);
   a.units = Qdesc->rows * a.cpr;
-  if (mx_quant_blocks(a.units) > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (mx_quant_blocks(a.units, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (!h->online) return QG_ERR_HIP;
   return launch_mx_quantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
@@ -1084,9 +1084,9 @@ int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const 
   a.Y = Y;
   a.cpr = (int32_t)cdiv(Qdesc->cols, 8);
   a.units = Qdesc->rows * a.cpr;
-  if (mx_quant_blocks(a.units) > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (mx_quant_blocks(a.units, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (!h->online) return QG_ERR_HIP;
-  return launch_mx_dequantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+  return launch_mx_dequantize(a, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_plan(qg_handle* h, const qg_operation* op, const qg_layout* Adesc, const qg_layout* Udesc,

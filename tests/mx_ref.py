@@ -16,7 +16,7 @@ def quantise(x):
     rows, k = x.shape
     b = np.zeros((rows, up(k, 32)))
     b[:, :k] = x
-    b = b.reshape(rows, -1, 32)
+    b = b.reshape(rows, -(-k // 32), 32)
     bad = ~np.isfinite(b).all(-1)
     b = np.where(bad[..., None], 0.0, b)
     top = np.abs(b).max(-1)
@@ -29,7 +29,7 @@ def quantise(x):
     code |= ((b < 0) | ((b == 0) & np.signbit(b))).astype(np.uint8) << 3
     byte = np.where(bad, 255, byte).astype(np.uint8)
     code[bad] = 0
-    return code.reshape(rows, -1), byte
+    return code.reshape(rows, up(k, 32)), byte
 
 
 def pack(code):
