@@ -1086,7 +1086,7 @@ int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const 
   a.units = Qdesc->rows * a.cpr;
   if (mx_quant_blocks(a.units, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (!h->online) return QG_ERR_HIP;
-  return launch_mx_dequantize(a, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+  return launch_mx_dequantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_plan(qg_handle* h, const qg_operation* op, const qg_layout* Adesc, const qg_layout* Udesc,

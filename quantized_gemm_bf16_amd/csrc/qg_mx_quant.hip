@@ -208,53 +208,69 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const MxQuantArgs
       if (top >= 0x7F800000u) q = 0, byte = 255;
     }
     if (live[i]) {
-      __builtin_nontemporal_store(q, (uint32_t*)(a.Q + at[i].row * a.ldq + at[i].unit * 4));
+      *(uint32_t*)(a.Q + at[i].row * a.ldq + at[i].unit * 4) = q;
       if ((threadIdx.x & 3) == 0) a.S[at[i].row * a.lds + (at[i].unit >> 2)] = (char)byte;
     }
   }
 }
 
-template <int DT>
+// The values go out past the L2 (non-temporal): they are many times what it
+// holds, and it keeps the codes that are still to be read instead.
+template <int DT, int U>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantArgs a) {
-  const int64_t first = (int64_t)blockIdx.x * kThreads;
-  const Place at = Places(first, a.cpr).at(threadIdx.x);
-  if (first + threadIdx.x >= a.units) return;
-  const uint32_t q = *(const uint32_t*)(a.Q + at.row * a.ldq + at.unit * 4);
-  const uint32_t s = (uint8_t)a.S[at.row * a.lds + (at.unit >> 2)];
-  // 2^(s - 127): byte 0 is fp32's subnormal 2^-127, byte 255 NaN
-  const float scale = __builtin_bit_cast(float, s == 255 ? 0x7FC00000u : s ? s << 23 : 0x00400000u);
-  float v[8];
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * U);
+  const Places places(first, a.cpr);
+  uint32_t q[U], s[U];
+  Place at[U];
+  bool live[U];
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const uint32_t b = q >> (8 * h);
-    const f32x2 y = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(b, 1.0f, 0);
-    v[2 * h] = y[0] * scale;
-    v[2 * h + 1] = y[1] * scale;
-  }
-  const int k = at.unit * 8;
-  const int64_t base = at.row * a.ldx + k;
-  if constexpr (DT == DT_F32) {
-    float* y = (float*)a.Y + base;
-    if (k + 8 <= a.K) {
-      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)y);
-      __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)y + 1);
-    } else {
-      for (int j = 0; j < 8; ++j)
-        if (k + j < a.K) y[j] = v[j];
+  for (int i = 0; i < U; ++i) {
+    const uint32_t off = i * kThreads + threadIdx.x;
+    live[i] = first + off < a.units;
+    at[i] = places.at(off);
+    q[i] = s[i] = 0;
+    if (live[i]) {
+      q[i] = *(const uint32_t*)(a.Q + at[i].row * a.ldq + at[i].unit * 4);
+      s[i] = (uint8_t)a.S[at[i].row * a.lds + (at[i].unit >> 2)];
     }
-  } else {
-    uint16_t* y = (uint16_t*)a.Y + base;
-    uint32_t h[8];
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = DT == DT_BF16 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
-    if (k + 8 <= a.K) {
-      const i32x4 p = {(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16),
-                       (int)(h[6] | h[7] << 16)};
-      __builtin_nontemporal_store(p, (i32x4*)y);
+  for (int i = 0; i < U; ++i) {
+    if (!live[i]) continue;
+    // 2^(s - 127): byte 0 is fp32's subnormal 2^-127, byte 255 NaN
+    const float scale = __builtin_bit_cast(float, s[i] == 255 ? 0x7FC00000u : s[i] ? s[i] << 23 : 0x00400000u);
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      typedef float f32x2 __attribute__((ext_vector_type(2)));
+      const f32x2 y = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[i] >> (8 * h), 1.0f, 0);
+      v[2 * h] = y[0] * scale;
+      v[2 * h + 1] = y[1] * scale;
+    }
+    const int k = at[i].unit * 8;
+    const int64_t base = at[i].row * a.ldx + k;
+    if constexpr (DT == DT_F32) {
+      float* y = (float*)a.Y + base;
+      if (k + 8 <= a.K) {
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)y);
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)y + 1);
+      } else {
+        for (int j = 0; j < 8; ++j)
+          if (k + j < a.K) y[j] = v[j];
+      }
     } else {
-      for (int j = 0; j < 8; ++j)
-        if (k + j < a.K) y[j] = (uint16_t)h[j];
+      uint16_t* y = (uint16_t*)a.Y + base;
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = DT == DT_BF16 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
+      if (k + 8 <= a.K) {
+        const i32x4 p = {(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16),
+                         (int)(h[6] | h[7] << 16)};
+        __builtin_nontemporal_store(p, (i32x4*)y);
+      } else {
+        for (int j = 0; j < 8; ++j)
+          if (k + j < a.K) y[j] = (uint16_t)h[j];
+      }
     }
   }
 }
@@ -264,21 +280,25 @@ hipError_t quantize_u(const MxQuantArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((mx_quantize_kernel<DT, GATED, U>), dim3((unsigned)mx_quant_blocks(a.units, U)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
-// Two units per lane, for more loads in flight, once that still leaves every
-// CU eight workgroups (4096 rows gathered to 32768 x 7168: 89 us, 99 with one,
-// 85 with four; 8192 x 14336 gated: 95 and 98); one below, so that few rows spread wide.
-template <int DT, bool GATED>
-hipError_t quantize_g(const MxQuantArgs& a, int cus, hipStream_t s) {
-  return a.units >= (int64_t)cus * 8 * 2 * kThreads ? quantize_u<DT, GATED, 2>(a, s) : quantize_u<DT, GATED, 1>(a, s);
-}
+// Several units per lane, for more loads in flight, once that still leaves
+// every CU eight workgroups; one below, so that few rows spread wide. 4096 rows
+// gathered to 32768 x 7168 and back: 178 us with four units both ways, 183 with
+// two, 209 with one; 8192 x 14336 gated and back: 149 us with two, 151 to 155 with one.
+bool several(const MxQuantArgs& a, int cus, int per_lane) { return a.units >= (int64_t)cus * 8 * per_lane * kThreads; }
+
 template <int DT>
 hipError_t quantize_t(const MxQuantArgs& a, int cus, hipStream_t s) {
-  return a.swiglu ? quantize_g<DT, true>(a, cus, s) : quantize_g<DT, false>(a, cus, s);
+  if (a.swiglu) return several(a, cus, 2) ? quantize_u<DT, true, 2>(a, s) : quantize_u<DT, true, 1>(a, s);
+  return several(a, cus, 4) ? quantize_u<DT, false, 4>(a, s) : quantize_u<DT, false, 1>(a, s);
+}
+template <int DT, int U>
+hipError_t dequantize_u(const MxQuantArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((mx_dequantize_kernel<DT, U>), dim3((unsigned)mx_quant_blocks(a.units, U)), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
 }
 template <int DT>
-hipError_t dequantize_t(const MxQuantArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(mx_dequantize_kernel<DT>, dim3((unsigned)mx_quant_blocks(a.units, 1)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+hipError_t dequantize_t(const MxQuantArgs& a, int cus, hipStream_t s) {
+  return several(a, cus, 4) ? dequantize_u<DT, 4>(a, s) : dequantize_u<DT, 1>(a, s);
 }
 
 }  // namespace
@@ -294,11 +314,11 @@ hipError_t launch_mx_quantize(const MxQuantArgs& a, int cus, hipStream_t s) {
   }
 }
 
-hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s) {
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, int cus, hipStream_t s) {
   switch (a.x_type) {
-    case DT_F32: return dequantize_t<DT_F32>(a, s);
-    case DT_F16: return dequantize_t<DT_F16>(a, s);
-    case DT_BF16: return dequantize_t<DT_BF16>(a, s);
+    case DT_F32: return dequantize_t<DT_F32>(a, cus, s);
+    case DT_F16: return dequantize_t<DT_F16>(a, cus, s);
+    case DT_BF16: return dequantize_t<DT_BF16>(a, cus, s);
     default: return hipErrorInvalidValue;
   }
 }

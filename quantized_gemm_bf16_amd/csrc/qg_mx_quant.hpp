@@ -21,7 +21,7 @@ struct MxQuantArgs {
 };
 
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int cus, hipStream_t s);
-hipError_t launch_mx_dequantize(const MxQuantArgs& a, hipStream_t s);
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, int cus, hipStream_t s);
 // Workgroups of a launch that takes `per_lane` units per lane (one at least, so
 // that at one they bound what the engine may launch).
 int64_t mx_quant_blocks(int64_t units, int per_lane);
