@@ -334,6 +334,16 @@ struct Mx : Tile<Cfg> {
     for (; kt < u.ke; ++kt) step(std::false_type{}, kt);
     __syncthreads();
   }
+
+  __device__ __forceinline__ static void store(const Args& a, const Unit& u, Acc& acc, char* smem) {
+    if constexpr (Base::STAGED) {
+      if (Base::plain16(a)) {
+        Base::template store_staged<false>(a, u, acc, smem);
+        return;
+      }
+    }
+    Base::store(a, u, acc, smem);
+  }
 };
 
 template <class Cfg>

@@ -476,6 +476,9 @@ struct Tile {
     return (a.d_type == DT_BF16 || a.d_type == DT_F16) && (a.c_type < 0 || a.beta == 0.f) && a.epi == 0;
   }
 
+  // DRAIN: the call ends only when the stores have completed; without, they
+  // drain behind the next unit's loads.
+  template <bool DRAIN = true>
   __device__ __forceinline__ static void store_staged(const Args& a, const Unit& u, Acc& acc, char* smem) {
     const int w = wave_id(), l = lane_id();
     const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
@@ -519,7 +522,11 @@ struct Tile {
           if (n + j < a.N) p[j] = hv[j];
       }
     }
-    __syncthreads();  // the staging area is the next unit's ring
+    // the staging area is the next unit's ring
+    if constexpr (DRAIN)
+      __syncthreads();
+    else
+      lds_barrier();
   }
 
   // Final results of a tile: epilogue + masked store.
