@@ -627,7 +627,7 @@ Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws
   static const struct {
     int side;
     double fixed, alone, step;
-  } kTiles[] = {{64, 1.1, 0.3, 0.25}, {128, 3.5, 0.65, 0.75}, {256, 7.5, 2.4, 2.4}};
+  } kTiles[] = {{64, 1.1, 0.3, 0.27}, {128, 3.5, 0.65, 0.75}, {256, 7.5, 2.4, 2.4}};
   const double steps = (double)cdiv(p.K, 256);
   double best = 0;
   for (const auto& t : kTiles) {

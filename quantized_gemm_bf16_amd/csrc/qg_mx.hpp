@@ -124,6 +124,10 @@ struct Mx : Tile<Cfg> {
   using Acc = typename Base::Acc;
   static constexpr int TM = Cfg::TM, TN = Cfg::TN, BM = Cfg::BM, BN = Cfg::BN, NT = Cfg::NT;
   static constexpr int SMEM_BYTES = Cfg::RING + Cfg::SPANS * Cfg::SPAN;
+  // Grouped, 256 x 256 tiles: an XCD's tiles share their rows of A and B in its
+  // L2 (64 experts, 16384 rows, N 2048, K 7168: 227 us, 237 without; 128 x 128
+  // tiles, bound by other things than the L2's misses, 272 and 250).
+  static constexpr bool GROUPED_XCD = BM == 256;
 
   __device__ __forceinline__ static void mainloop(const Args& a, const Unit& u, char* smem, Acc& acc) {
     const int w = wave_id(), l = lane_id();

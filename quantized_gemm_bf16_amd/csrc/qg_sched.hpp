@@ -38,6 +38,17 @@ struct Unit {
   int kb, ke;       // k-tile range [kb, ke)
 };
 
+// Whether a core's grouped units are dealt to the XCDs in contiguous ranges
+// (Core::GROUPED_XCD) or one by one (cores that do not say).
+template <class Core, class = void>
+struct GroupedXcd {
+  static constexpr bool value = false;
+};
+template <class Core>
+struct GroupedXcd<Core, decltype((void)Core::GROUPED_XCD)> {
+  static constexpr bool value = Core::GROUPED_XCD;
+};
+
 template <class Core>
 struct Sched {
   using Acc = typename Core::Acc;
@@ -293,7 +304,13 @@ struct Sched {
     }
     const int mtiles = batched ? a.E * a.tiles_m : pref[a.E];
     const int total = mtiles * a.tiles_n;
-    for (int b = blockIdx.x; b < total; b += gridDim.x) {
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+      int b = i;
+      if constexpr (GroupedXcd<Core>::value) {
+        // within each round of the persistent loop, as in run_dp
+        const int round = i - blockIdx.x;
+        b = round + xcd_remap(blockIdx.x, min((int)gridDim.x, total - round));
+      }
       const int mt = b / a.tiles_n, tn = b - mt * a.tiles_n;
       Unit u;
       if (batched) {
