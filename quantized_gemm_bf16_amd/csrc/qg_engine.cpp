@@ -604,14 +604,16 @@ int skinny_for(const Problem& p, int64_t target_bn) {
 // to 32 its wider form while one workgroup per 16 columns fits on the CUs
 // (32 x 4096 x 14336: 11.8 against 13.4; N = 8192: 20 against 16.8), experts with
 // up to 4 rows on average the one that shares A (64 experts, 128 rows, N 2048,
-// K 7168: 85 us, 64 x 64 tiles 88, 128 x 128 tiles 98). Otherwise the square tile
-// with the least estimated time: a CU that has n tiles takes n (fixed + step per
-// 256 of K), step being less for a tile that has the CU to itself and no
-// neighbour to share the L2 with. Measured, us, tiles of 64 / 128 / 256:
-//   128 x 4096 x 4096       8.9 /  14 /   -      512 x 8192 x 8192        36 /  25 /   -
-//   4096 x 4096 x 4096       73 /  53 /  48      64 experts, 1024 rows    98 / 102 /   -
-//   64 experts, 4096 rows   137 / 130 / 148      16384 rows              336 / 250 / 237
-//   8 experts, 16384 rows, N 4096, K 1000        139 / 119 /  86
+// K 7168: 85 us, 64 x 64 tiles 88, 128 x 128 tiles 98). Otherwise the tile with
+// the least estimated time: a CU that has n tiles takes n (fixed + step per 256
+// of K), step being less for a tile that has the CU to itself. 64 x 32 tiles,
+// whose two groups of waves fill a CU, are for products of up to one tile per
+// CU. Measured, us, tiles of 64 x 32 / 64 / 128 / 256:
+//   64 x 8192 x 8192     11.2 / 13.8 /  20 /   -     333 x 1001 x 2075       7.9 / 8.2 /  13 /   -
+//   512 x 8192 x 8192      48 /   37 /  26 /  56     4096 x 4096 x 4096        - /  78 /  59 /  44
+//   64 experts, N 2048, K 7168: 1024 rows            - /  98 / 102 / 135     4096 rows   - / 138 / 130 / 139
+//                              16384 rows            - / 337 / 250 / 222
+//   8 experts, 16384 rows, N 4096, K 1000            - / 148 / 121 /  81
 Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, int forced_mode) {
   Choice c;
   const double cus = h->cus;
@@ -625,31 +627,31 @@ Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws
   }
   if (c.kernel >= 0) return c;
   static const struct {
-    int side;
+    int bm, bn;
     double fixed, alone, step;
-  } kTiles[] = {{64, 1.1, 0.3, 0.27}, {128, 3.5, 0.65, 0.75}, {256, 7.5, 2.4, 2.4}};
+  } kTiles[] = {{64, 32, 1.5, 0.17, 0}, {64, 64, 1.1, 0.3, 0.27}, {128, 128, 3.5, 0.65, 0.75}, {256, 256, 7.5, 2.4, 2.4}};
   const double steps = (double)cdiv(p.K, 256);
-  double best = 0;
+  double best = 0, step = 0;
   for (const auto& t : kTiles) {
     // m-tiles: exact, or with every expert that has rows ending inside a tile half the time
     const double live = (double)std::min<int64_t>(p.E, p.M);
-    const double tm = grouped ? std::max(live, (double)cdiv(p.M, t.side) + live / 2)
-                              : (double)cdiv(p.M, t.side) * (p.batched ? p.E : 1);
-    const double n = std::max(1.0, std::ceil(tm * (double)cdiv(p.N, t.side) / cus));
+    const double tm = grouped ? std::max(live, (double)cdiv(p.M, t.bm) + live / 2)
+                              : (double)cdiv(p.M, t.bm) * (p.batched ? p.E : 1);
+    const double n = std::max(1.0, std::ceil(tm * (double)cdiv(p.N, t.bn) / cus));
+    if (t.step == 0 && (n > 1 || p.E > 0)) continue;
     const double us = n * (t.fixed + steps * (n > 1 ? t.step : t.alone));
     if (c.kernel >= 0 && us >= best) continue;
-    const int k = kernel_by_shape(p, t.side, t.side);
-    if (k >= 0) c.kernel = k, best = us;
+    const int k = kernel_by_shape(p, t.bm, t.bn);
+    if (k >= 0) c.kernel = k, best = us, step = t.alone;
   }
   // A long K over few tiles: up to eight chunks that fit on the CUs together,
-  // four k-tiles each at least, where they save more than the 5 us that the
-  // partial tiles cost (64 x 1024 x 14336: 11.1 us in eight chunks, 20 whole,
-  // 13.5 in fourteen).
+  // four k-tiles each at least, where they save more than the 4 us that the
+  // partial tiles cost (64 x 1024 x 14336: 10.9 us in eight chunks, 14 whole).
   if (c.kernel < 0 || p.E > 0 || forced_mode >= 0 || !ws || !ws->partials || !ws->barriers) return c;
   const KernelInfo& k = kKernels[c.kernel];
   const int64_t tiles = cdiv(p.M, k.bm) * cdiv(p.N, k.bn), iters = cdiv(p.K, k.bk);
   const int64_t s = std::min<int64_t>({8, h->cus / std::max<int64_t>(tiles, 1), iters / 4});
-  if (k.bm == 64 && s > 1 && 0.3 * (double)(iters - cdiv(iters, s)) > 5 &&
+  if (k.bm == 64 && s > 1 && step * (double)(iters - cdiv(iters, s)) > 4 &&
       (size_t)tiles * s * k.slot_bytes <= ws->partials_size && (size_t)tiles * 4 <= ws->barriers_size) {
     c.mode = MODE_SPLITK;
     c.split = (int)s;

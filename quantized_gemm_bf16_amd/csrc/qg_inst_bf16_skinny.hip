@@ -14,7 +14,7 @@ namespace qg {
   template hipError_t launch_skinny<SkinnyCfg<El::BF16, BN, NW, MT, DP, BB, NS>>(const Args&, int, hipStream_t);
 #define QG_W4(MT, BN, WN, WK, ST)
 #define QG_F8(BM, BN, WM, WN, ST)
-#define QG_MX(BM, BN, WM, WN, ST, RB)
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK)
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH)
 #include "qg_kernel_list.inc"
 }  // namespace qg

@@ -13,7 +13,7 @@ namespace qg {
 #define QG_W4(MT, BN, WN, WK, ST)
 #define QG_F8(BM, BN, WM, WN, ST) \
   template hipError_t launch_f8<F8Cfg<BM, BN, WM, WN, ST>>(const Args&, int, hipStream_t);
-#define QG_MX(BM, BN, WM, WN, ST, RB)
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK)
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH)
 #include "qg_kernel_list.inc"
 }  // namespace qg

@@ -11,8 +11,8 @@ namespace qg {
 #define QG_SKINNY_I8(BN, NW, MT, DP, BB, NS)
 #define QG_W4(MT, BN, WN, WK, ST)
 #define QG_F8(BM, BN, WM, WN, ST)
-#define QG_MX(BM, BN, WM, WN, ST, RB) \
-  template hipError_t launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>(const Args&, int, hipStream_t);
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK) \
+  template hipError_t launch_mx<MxCfg<BM, BN, WM, WN, ST, RB, WK>>(const Args&, int, hipStream_t);
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH)
 #include "qg_kernel_list.inc"
 }  // namespace qg

@@ -11,7 +11,7 @@ namespace qg {
 #define QG_SKINNY_I8(BN, NW, MT, DP, BB, NS)
 #define QG_W4(MT, BN, WN, WK, ST)
 #define QG_F8(BM, BN, WM, WN, ST)
-#define QG_MX(BM, BN, WM, WN, ST, RB)
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK)
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH) \
   template hipError_t launch_mx_skinny<MxSkinnyCfg<BN, NW, MT, DP, SH>>(const Args&, int, hipStream_t);
 #include "qg_kernel_list.inc"

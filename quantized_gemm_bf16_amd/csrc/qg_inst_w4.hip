@@ -12,7 +12,7 @@ namespace qg {
 #define QG_W4(MT, BN, WN, WK, ST) \
   template hipError_t launch_w4<W4Cfg<MT, BN, WN, WK, ST>>(const Args&, int, hipStream_t);
 #define QG_F8(BM, BN, WM, WN, ST)
-#define QG_MX(BM, BN, WM, WN, ST, RB)
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK)
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH)
 #include "qg_kernel_list.inc"
 }  // namespace qg

@@ -101,21 +101,28 @@ __device__ __forceinline__ int pinned_lane(int x) {
 //    row, A's rows and then B's, two of them loaded together: what the L2 can
 //    serve is a number of requests, and a k-tile's 4 or 8 bytes of scales of a
 //    row would cost it as much as the row's 64 or 128 bytes of codes.
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int ROWB_>
-struct MxCfg : TileCfg<El::E4M3, BM_, BN_, WM_, WN_, STAGES_, ROWB_> {
-  using Base = TileCfg<El::E4M3, BM_, BN_, WM_, WN_, STAGES_, ROWB_>;
+//  - a wave alone on its SIMD issues an instruction every four cycles or more,
+//    and a small tile has one wave per SIMD and few tiles: WAVES_K groups of
+//    waves, each with rings of its own, share the tile's k-tiles in contiguous
+//    halves, and their sums meet in LDS at the end, in order.
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int ROWB_, int WK_>
+struct MxCfg : TileCfg<El::E4M3, BM_, BN_, WM_, WN_, 2, ROWB_> {
+  using Base = TileCfg<El::E4M3, BM_, BN_, WM_, WN_, 2, ROWB_>;
+  static constexpr int STAGES = STAGES_;         // (the base's bounds are those of its own load issue)
+  static constexpr int WAVES_K = WK_, NT = Base::NW * WK_ * 64;
   static constexpr int BK = 2 * ROWB_;           // codes per k-tile
   static constexpr int KS = ROWB_ / 32;          // MFMAs along k per k-tile
   static constexpr int KPS = 256 / ROWB_;        // k-tiles per span of scales
-  static constexpr int GA = BM_ / 64, GT = (BM_ + BN_) / 64;  // 64-row scale loads per span: of A, in all
-  static constexpr int SPAN = (BM_ + BN_) * 16;
+  static constexpr int GA = BM_ / 64, GT = GA + (BN_ + 63) / 64;  // 64-row scale loads per span: of A, in all
+  static constexpr int SPAN = GT * 1024;
   static constexpr int RING = STAGES_ * Base::STAGE_BYTES;
-  static_assert(BM_ % 64 == 0 && BN_ % 64 == 0 && GT <= Base::NW, "a wave loads the scales of 64 rows");
+  static_assert(BM_ % 64 == 0 && GT <= Base::NW, "a wave loads the scales of 64 rows");
   // Spans in the ring, and how many before their own two are loaded: a wave's
   // loads are known to have landed STAGES - 2 k-tiles after the one that they went out in.
-  static constexpr int SPANS = KPS >= STAGES_ - 1 ? 3 : 4, LEAD = SPANS - 2;
-  static_assert(STAGES_ >= 2 && LEAD * KPS >= STAGES_ - 1, "scales land in the k-tiles between their load and their use");
-  static_assert(RING + SPANS * SPAN <= 160 * 1024 - 4352, "LDS budget");
+  static constexpr int LEAD = (STAGES_ - 1 + KPS - 1) / KPS, SPANS = LEAD + 2;
+  static_assert(STAGES_ >= 2 && Base::LPW * (STAGES_ - 1) + SPANS < 64, "vmcnt range");
+  static constexpr int GROUP_BYTES = RING + SPANS * SPAN;  // LDS of one group of waves
+  static_assert(WK_ * GROUP_BYTES <= 160 * 1024 - 4352 && BM_ * BN_ * 4 * (WK_ - 1) <= WK_ * GROUP_BYTES, "LDS budget");
 };
 
 template <class Cfg>
@@ -123,14 +130,24 @@ struct Mx : Tile<Cfg> {
   using Base = Tile<Cfg>;
   using Acc = typename Base::Acc;
   static constexpr int TM = Cfg::TM, TN = Cfg::TN, BM = Cfg::BM, BN = Cfg::BN, NT = Cfg::NT;
-  static constexpr int SMEM_BYTES = Cfg::RING + Cfg::SPANS * Cfg::SPAN;
+  static constexpr int SMEM_BYTES = Cfg::WAVES_K * Cfg::GROUP_BYTES;
+  static constexpr int WK = Cfg::WAVES_K;
   // Grouped, 256 x 256 tiles: an XCD's tiles share their rows of A and B in its
   // L2 (64 experts, 16384 rows, N 2048, K 7168: 227 us, 237 without; 128 x 128
   // tiles, bound by other things than the L2's misses, 272 and 250).
   static constexpr bool GROUPED_XCD = BM == 256;
 
-  __device__ __forceinline__ static void mainloop(const Args& a, const Unit& u, char* smem, Acc& acc) {
-    const int w = wave_id(), l = lane_id();
+  // Waves of the first group hold the tile once the mainloop has ended.
+  __device__ __forceinline__ static bool holds_partial() { return WK == 1 || wave_id() < Cfg::NW; }
+
+  __device__ __forceinline__ static void mainloop(const Args& a, const Unit& unit, char* smem0, Acc& acc) {
+    const int group = WK == 1 ? 0 : wave_id() / Cfg::NW;
+    const int share = (unit.ke - unit.kb + WK - 1) / WK;  // k-tiles of a group; the last ones may have fewer
+    Unit u = unit;
+    u.kb = min(unit.ke, unit.kb + group * share);
+    u.ke = min(unit.ke, u.kb + share);
+    char* smem = smem0 + group * Cfg::GROUP_BYTES;
+    const int w = WK == 1 ? wave_id() : wave_id() % Cfg::NW, l = lane_id();
     const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
     const int64_t lda_b = a.lda / 2, ldb_b = a.ldb / 2;
     const uint32_t K = (uint32_t)a.K;
@@ -260,65 +277,73 @@ struct Mx : Tile<Cfg> {
       for (int tm = 0; tm < TM; ++tm) acc.v[tn][tm] = f32x16{};
 
     // The k-tiles before `fast` prefetch a whole k-tile and find nothing to
-    // trim in the next one; they wait for the next stage's loads only
-    // (counting codes: where scales were loaded since, for a load more). The
-    // last ones wait for all of what is left.
-    constexpr int S = Cfg::STAGES;
+    // trim in the next one.
+    constexpr int S = Cfg::STAGES, P = S - 1;  // k-tiles under way
     const int whole = min(u.ke, (int)(K / (2 * ROWB)));  // k-tiles [kb, whole) are whole
-    int fast = whole - S + 1;
+    int fast = whole - P;
     if (tail_scales >= 0) fast = min(fast, tail_scales - 1);
     fast = max(fast, u.kb);
+    // Waits until at most the code loads of the last n k-tiles are under way
+    // (scales loaded among them make it wait for a load or two more).
+    auto wait_tiles = [&](int n) {
+      static_for<P>([&](auto N) {
+        if (n == decltype(N)::value) wait_vmcnt<LPW * decltype(N)::value>();
+      });
+    };
     load_spans(u.kb / KPS, ((u.kb / KPS + LEAD) & ~1) + 2);  // all that no later k-tile of the unit loads
 #pragma unroll
-    for (int st = 0; st < S - 1; ++st)
+    for (int st = 0; st < P; ++st)
       if (u.kb + st < u.ke) load_tile(st, u.kb + st);
-    if (u.kb + S - 1 <= u.ke)
-      wait_vmcnt<LPW*(S - 2)>();
-    else
-      wait_vmcnt<0>();
+    wait_tiles(max(0, min(u.ke - u.kb, P) - 1));
     if (u.kb == tail_codes || u.kb == tail_scales) trim(0, u.kb);
     lds_barrier();
+    constexpr int NM = TM * TN;  // MFMAs of a k-step
+    int kt = u.kb, st = 0;       // the k-tile and its stage
+    // Meets the other waves once k-tile kt + 1 has landed.
+    auto publish = [&](auto FAST, int kt, int next) {
+      if constexpr (decltype(FAST)::value) {
+        wait_vmcnt<LPW*(S - 2)>();
+      } else {
+        wait_tiles(max(0, min(u.ke, kt + S) - (kt + 2)));
+        if (kt + 1 == tail_codes || kt + 1 == tail_scales) trim(next, kt + 1);
+      }
+      lds_barrier();
+    };
+
+    constexpr int EARLY = NM / 2;  // MFMAs of the last k-step before the barrier
     Frags cur;
     Scales sc;
     read_frags(0, 0, cur);
-    read_scales(u.kb, sc);
+    read_scales(kt, sc);
     half_scales(sc);
-    int st = 0, ahead = S - 1;  // stages of k-tile kt and of the one being loaded
-    constexpr int NM = TM * TN, EARLY = NM / 2;  // MFMAs of a k-step; those of the last one before the barrier
-    auto step = [&](auto FAST, int kt) {
+    int ahead = S - 1;  // stage of the k-tile being loaded
+    auto step = [&](auto FAST) {
       constexpr bool F = decltype(FAST)::value;
       const int next = st + 1 == S ? 0 : st + 1;
       load_next_spans(kt);
       if constexpr (!F)
-        if (kt + S - 1 < u.ke) load_tile(ahead, kt + S - 1);
+        if (kt + P < u.ke) load_tile(ahead, kt + P);
       static_for<KS>([&](auto KI) {
         constexpr int ks = decltype(KI)::value;
         constexpr bool last = ks + 1 == KS;
         Frags nxt;
         Scales ns;
         if constexpr (!last) read_frags(st, ks + 1, nxt);
-        // Loads [l0, l1) of the k-tile ahead go out in this k-step, in the last
-        // one before the barrier. With two stages that k-tile is the next one:
-        // its loads go out in the first half, the second half lets them land.
-        constexpr int LK = S == 2 ? KS / 2 : KS;
-        constexpr int l0 = ks < LK ? LPW * ks / LK : LPW, l1 = ks < LK ? LPW * (ks + 1) / LK : LPW, room = last ? EARLY : NM;
+        // loads [l0, l1) go out in this k-step, in the last one before the barrier
+        constexpr int l0 = LPW * ks / KS, l1 = LPW * (ks + 1) / KS, room = last ? EARLY : NM;
         static_for<NM>([&](auto MI) {
           constexpr int m = decltype(MI)::value, tn = m / TM, tm = m % TM;
           if constexpr (F) {
             static_for<l1 - l0>([&](auto LI) {
               constexpr int j = decltype(LI)::value;
               if constexpr (j * room / (l1 - l0) == m) {
-                load(std::true_type{}, l0 + j, ahead, kt + S - 1, l);
+                load(std::true_type{}, l0 + j, ahead, kt + P, l);
                 __builtin_amdgcn_sched_barrier(0);
               }
             });
           }
           if constexpr (last && m == EARLY) {
-            // the next stage has landed and every wave has read this one
-            wait_vmcnt<F ? LPW*(S - 2) : 0>();
-            if constexpr (!F)
-              if (kt + 1 == tail_codes || kt + 1 == tail_scales) trim(next, kt + 1);
-            lds_barrier();
+            publish(FAST, kt, next);
             read_frags(next, 0, nxt);
             read_scales(kt + 1, ns);
           }
@@ -332,21 +357,46 @@ struct Mx : Tile<Cfg> {
       });
       ahead = st;
       st = next;
+      ++kt;
     };
-    int kt = u.kb;
-    for (; kt < fast; ++kt) step(std::true_type{}, kt);
-    for (; kt < u.ke; ++kt) step(std::false_type{}, kt);
+    while (kt < fast) step(std::true_type{});
+    while (kt < u.ke) step(std::false_type{});
+    for (int i = u.ke - u.kb; i < share; ++i) lds_barrier();  // the barriers of a group with more k-tiles
     __syncthreads();
+    if constexpr (WK > 1) {
+      // the groups' sums, in k order, to the first group
+      f32x4* red = (f32x4*)smem0;
+      if (group > 0) {
+#pragma unroll
+        for (int c = 0; c < Base::NCH; ++c) red[(((group - 1) * Base::NCH + c) * Cfg::NW + w) * 64 + l] = Base::get4(acc, c);
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int g = 0; g < WK - 1; ++g)
+#pragma unroll
+          for (int c = 0; c < Base::NCH; ++c)
+            Base::set4(acc, c, Base::get4(acc, c) + red[((g * Base::NCH + c) * Cfg::NW + w) * 64 + l]);
+      }
+      __syncthreads();
+    }
+  }
+
+  __device__ __forceinline__ static void write_partial(const Args& a, int slot, Acc& acc) {
+    if (holds_partial()) Base::write_partial(a, slot, acc);
   }
 
   __device__ __forceinline__ static void store(const Args& a, const Unit& u, Acc& acc, char* smem) {
     if constexpr (Base::STAGED) {
       if (Base::plain16(a)) {
-        Base::template store_staged<false>(a, u, acc, smem);
+        if (holds_partial())
+          Base::template store_staged<false>(a, u, acc, smem);
+        else
+          lds_barrier();  // the one that ends it
         return;
       }
     }
-    Base::store(a, u, acc, smem);
+    if (holds_partial()) Base::store(a, u, acc, smem);
   }
 };
 

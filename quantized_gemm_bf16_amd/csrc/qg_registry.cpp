@@ -22,8 +22,8 @@ namespace qg {
   extern template hipError_t launch_w4<W4Cfg<MT, BN, WN, WK, ST>>(const Args&, int, hipStream_t);
 #define QG_F8(BM, BN, WM, WN, ST) \
   extern template hipError_t launch_f8<F8Cfg<BM, BN, WM, WN, ST>>(const Args&, int, hipStream_t);
-#define QG_MX(BM, BN, WM, WN, ST, RB) \
-  extern template hipError_t launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>(const Args&, int, hipStream_t);
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK) \
+  extern template hipError_t launch_mx<MxCfg<BM, BN, WM, WN, ST, RB, WK>>(const Args&, int, hipStream_t);
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH) \
   extern template hipError_t launch_mx_skinny<MxSkinnyCfg<BN, NW, MT, DP, SH>>(const Args&, int, hipStream_t);
 #include "qg_kernel_list.inc"
@@ -64,10 +64,10 @@ namespace qg {
   {"f8_E4M3_" #BM "x" #BN "_w" #WM "x" #WN "_s" #ST, FAM_F8, DT_E4M3, BM, BN, 128, ST, WM * WN * 64, BM * BN * 4, \
    &launch_f8<F8Cfg<BM, BN, WM, WN, ST>>},
 
-#define QG_MX(BM, BN, WM, WN, ST, RB)                                                                      \
-  {"mx_" #BM "x" #BN "x" #RB "b_w" #WM "x" #WN "_s" #ST, FAM_MX, DT_E2M1, BM, BN,                          \
-   MxCfg<BM, BN, WM, WN, ST, RB>::BK, ST, MxCfg<BM, BN, WM, WN, ST, RB>::NT, BM * BN * 4,                  \
-   &launch_mx<MxCfg<BM, BN, WM, WN, ST, RB>>},
+#define QG_MX(BM, BN, WM, WN, ST, RB, WK)                                                                      \
+  {"mx_" #BM "x" #BN "x" #RB "b_w" #WM "x" #WN "x" #WK "_s" #ST, FAM_MX, DT_E2M1, BM, BN,                          \
+   MxCfg<BM, BN, WM, WN, ST, RB, WK>::BK, ST, MxCfg<BM, BN, WM, WN, ST, RB, WK>::NT, BM * BN * 4,                  \
+   &launch_mx<MxCfg<BM, BN, WM, WN, ST, RB, WK>>},
 
 #define QG_MX_SKINNY(BN, NW, MT, DP, SH)                                                                       \
   {"mx_skinny_" #MT "x16x" #BN "_w" #NW "_d" #DP "_" #SH, FAM_MX_SKINNY, DT_E2M1, 16 * MT, BN,                  \
