@@ -91,20 +91,28 @@ __device__ __forceinline__ int pinned_lane(int x) {
 
 // ---- tiles ------------------------------------------------------------------
 // The LDS ring, swizzle and epilogue of the tile core, with ROWB bytes (2 ROWB
-// codes) of each row per stage. What bounds the loop is less the 32 cycles of
-// an instruction than feeding it: a stage's loads pass the CU's address unit
-// at 64 bytes a cycle, and a wave that issues them in a row stands still as
-// long. So
+// codes) of each row per stage. Large products are bound by power: 4096^3
+// takes 42 us (3.27 PFLOP/s) at a shader clock of 1.8 GHz, of which an MFMA-only
+// copy of the loop takes 25 and a launch and the stores 8, and a grouped prompt
+// (64 experts, 65536 x 2048 x 7168) 660 us; small ones by the latency of
+// their few k-tiles. What the loop does about both:
 //  - every wave issues its own loads one by one between its MFMAs, for the
-//    k-tile STAGES - 1 ahead, whose stage the last barrier freed;
+//    k-tile STAGES - 1 ahead, whose stage the last barrier freed: a wave that
+//    issues a stage's loads in a row stands still while they pass the address
+//    unit at 64 bytes a cycle (4096^3: 3860 instead of 4160 shader cycles per
+//    256 of k);
 //  - scales have a ring of their own, SPANS spans of 16 bytes (512 codes) per
 //    row, A's rows and then B's, two of them loaded together: what the L2 can
 //    serve is a number of requests, and a k-tile's 4 or 8 bytes of scales of a
-//    row would cost it as much as the row's 64 or 128 bytes of codes.
+//    row would cost it as much as the row's 64 or 128 bytes of codes (5180
+//    cycles);
 //  - a wave alone on its SIMD issues an instruction every four cycles or more,
 //    and a small tile has one wave per SIMD and few tiles: WAVES_K groups of
 //    waves, each with rings of its own, share the tile's k-tiles in contiguous
-//    halves, and their sums meet in LDS at the end, in order.
+//    halves, and their sums meet in LDS at the end, in order (64 x 8192 x 8192:
+//    10.3 us, 12.7 with one group).
+// The 256 x 256 tile takes 64-byte rows and four stages: with 128-byte rows only
+// two fit in LDS and the loop spills.
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int ROWB_, int WK_>
 struct MxCfg : TileCfg<El::E4M3, BM_, BN_, WM_, WN_, 2, ROWB_> {
   using Base = TileCfg<El::E4M3, BM_, BN_, WM_, WN_, 2, ROWB_>;

@@ -12,7 +12,11 @@
 // of a quad take one block, so the block maximum is two DPP exchanges and
 // nothing goes through LDS. Units are numbered row after row, whatever K is, so
 // that a wave is full at any width; a workgroup does one division to find its
-// first row and its lanes one multiplication each.
+// first row and its lanes one multiplication each. Measured, bf16: 8192 x 14336
+// gated 100 us (532 MB, 5.3 TB/s; a copy of 1 GiB reaches 5.15), 4096 rows
+// gathered to 32768 x 7168 92 us (each row read eight times, mostly from the
+// caches), the same codes back to values 85 us (594 MB, 7 TB/s: the codes come
+// from the memory-side cache), one row of 4096 2 us each way.
 //
 // SwiGLU: the codes are those of silu(g) * u without rounding before them, so
 // fp32 arithmetic alone would put values next to a rounding border on its

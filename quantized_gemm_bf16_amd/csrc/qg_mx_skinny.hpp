@@ -15,6 +15,11 @@
 // codes of one scale block; quarter l / 16 takes chunks 4 (l / 16) + s of the
 // block's 16 in step s, so that its four scales are one dword. B's rows are the
 // first operand: a lane ends up with 4 consecutive columns of one row of D.
+//
+// Measured: 1 x 4096 x 14336 k-interleaved in 8.3 us (31 MB: 3.8 TB/s with the
+// launch; the mainloops take 6.0), 64 experts of 2048 x 7168 with 128 rows
+// N-split in 84.7 us (477 MB: 5.6 TB/s, a plain streaming read 5.9). Four waves
+// and two blocks each: eight waves 9.4 us, 32 columns per workgroup 9.7.
 #pragma once
 #include "qg_mx.hpp"
 #include "qg_skinny.hpp"
