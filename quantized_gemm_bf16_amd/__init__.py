@@ -252,22 +252,22 @@ class Gemm:
 
     def mx_quantize_raw(self, X, Xd, Q, Qd, S, Sd, act=MX_IDENTITY, rows=None, stream=None) -> int:
         """qg_mx_quantize; returns the status code."""
-        return lib.qg_mx_quantize(self.h, int(act), _ptr(X), Xd, _ptr(rows), _ptr(Q), Qd, _ptr(S), Sd,
+        return lib.qg_mx_quantize(self.h, act, _ptr(X), Xd, _ptr(rows), _ptr(Q), Qd, _ptr(S), Sd,
                                   stream if stream is not None else _current_stream())
 
-    def mx_quantize(self, *args, **kw):
+    def mx_quantize(self, X, Xd, Q, Qd, S, Sd, act=MX_IDENTITY, rows=None, stream=None):
         """Rows of X (all, or those that the device int32 array `rows` names) to
         MXFP4 codes Q and scales S, through `act` (MX_IDENTITY, MX_SWIGLU)."""
-        _check(self.mx_quantize_raw(*args, **kw), "qg_mx_quantize")
+        _check(self.mx_quantize_raw(X, Xd, Q, Qd, S, Sd, act, rows, stream), "qg_mx_quantize")
 
     def mx_dequantize_raw(self, Q, Qd, S, Sd, Y, Yd, stream=None) -> int:
         """qg_mx_dequantize; returns the status code."""
         return lib.qg_mx_dequantize(self.h, _ptr(Q), Qd, _ptr(S), Sd, _ptr(Y), Yd,
                                     stream if stream is not None else _current_stream())
 
-    def mx_dequantize(self, *args, **kw):
-        """MXFP4 codes Q and scales S to the values they stand for."""
-        _check(self.mx_dequantize_raw(*args, **kw), "qg_mx_dequantize")
+    def mx_dequantize(self, Q, Qd, S, Sd, Y, Yd, stream=None):
+        """MXFP4 codes Q and scales S to the values Y that they stand for."""
+        _check(self.mx_dequantize_raw(Q, Qd, S, Sd, Y, Yd, stream), "qg_mx_dequantize")
 
     def plan(self, op, Ad, Ud, Bd, Vd, Cd, Dd, alpha, beta, ws=None) -> str:
         buf = ctypes.create_string_buffer(512)

@@ -211,3 +211,30 @@ def test_stream_and_graph(g):
         graph.replay()
         torch.cuda.synchronize()
         assert np.array_equal(y.double().cpu().numpy(), mx_ref.values(*mx_ref.quantise(mx_ref.swiglu(x))))
+
+
+def test_more_units_than_32_bits_count(g):
+    """2^32 units of 8 elements and more: 4.2 million rows of 8192, gathered from 16; codes, scales and values whole."""
+    k, n, t = 8192, (1 << 22) + 3001, 16
+    x = sample(t, k, "bf16", 4)
+    code, byte = mx_ref.quantise(x)
+    rows = torch.randint(0, t, (n,), device="cuda", dtype=torch.int32)
+    q = torch.empty(n, k // 2, dtype=torch.uint8, device="cuda")
+    s = torch.empty(n, k // 32, dtype=torch.uint8, device="cuda")
+    y = torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+    qd, sd = qg.layout("e2m1", n, k), qg.layout("e8m0", n, k // 32)
+    g.mx_quantize(pitched(x, "bf16"), qg.layout("bf16", t, k), q, qd, s, sd, rows=rows)
+    g.mx_dequantize(q, qd, s, sd, y, qg.layout("bf16", n, k))
+    values = torch.from_numpy(mx_ref.values(code, byte)).to(torch.bfloat16).cuda()
+    code, byte = torch.from_numpy(mx_ref.pack(code)).cuda(), torch.from_numpy(byte).cuda()
+    step = 1 << 18
+    for i in range(0, n, step):
+        r = rows[i:i + step].long()
+        assert torch.equal(s[i:i + step], byte[r])
+        assert torch.equal(y[i:i + step], values[r])
+        got, want = q[i:i + step], code[r]  # a code of zero may carry either sign
+        for nibble in (15, 240):
+            a, b = got & nibble, want & nibble
+            assert bool(((a == b) | ((a | b) & (nibble & 119) == 0)).all())
+    del q, s, y
+    torch.cuda.empty_cache()
