@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const MxQuantArgs
   }
 }
 
-// The values go out past the L2 (non-temporal): they are many times what it
+// 16-bit values go out past the L2 (non-temporal): they are many times what it
 // holds, and it keeps the codes that are still to be read instead.
 template <int DT, int U>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantArgs a) {
@@ -256,8 +256,9 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
     if constexpr (DT == DT_F32) {
       float* y = (float*)a.Y + base;
       if (k + 8 <= a.K) {
-        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)y);
-        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)y + 1);
+        // two accesses that each fill half of every line: merged in the L2
+        ((f32x4*)y)[0] = f32x4{v[0], v[1], v[2], v[3]};
+        ((f32x4*)y)[1] = f32x4{v[4], v[5], v[6], v[7]};
       } else {
         for (int j = 0; j < 8; ++j)
           if (k + j < a.K) y[j] = v[j];
