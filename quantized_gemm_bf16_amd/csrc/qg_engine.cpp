@@ -424,12 +424,13 @@ int mx_args(const void* vals, const qg_layout* Vd, int64_t vrows, int64_t vcols,
   if ((st = check_mx_operand(Q, Qd, Qd->rows, Qd->cols))) return st;
   if ((st = check_mx_operand(S, Sd, Qd->rows, cdiv(Qd->cols, 32)))) return st;
   if ((st = check_mx_operand(vals, Vd, vrows, vcols))) return st;
+  a.X = const_cast<void*>(vals);
   a.K = (int32_t)Qd->cols;
-  a.ldq = Qd->ld / 2;
-  a.lds = Sd->ld;
-  a.ldx = Vd->ld;
+  a.R = (int32_t)Qd->rows;
+  a.ldq = (int32_t)(Qd->ld / 2);
+  a.lds = (int32_t)Sd->ld;
+  a.ldx = (int32_t)Vd->ld;
   a.T = (int32_t)vrows;
-  a.x_type = Vd->type;
   a.Q = (char*)const_cast<void*>(Q);
   a.S = (char*)const_cast<void*>(S);
   return QG_OK;
@@ -1066,14 +1067,11 @@ int qg_mx_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc,
   if (st != QG_OK) return st;
   if (reinterpret_cast<uintptr_t>(rows) & 3) return QG_ERR_ALIGNMENT;
   if (Qdesc->rows == 0 || Qdesc->cols == 0) return QG_OK;
-  a.X = X;
   a.rows = rows;
-  a.swiglu = act == QG_MX_SWIGLU;
   a.cpr = (int32_t)(cdiv(Qdesc->cols, 32) * 4);
-  a.units = Qdesc->rows * a.cpr;
-  if (mx_quant_blocks(a.units, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (mx_quant_blocks(Qdesc->rows * a.cpr, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (!h->online) return QG_ERR_HIP;
-  return launch_mx_quantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+  return launch_mx_quantize(a, Xdesc->type, act == QG_MX_SWIGLU, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const void* S, const qg_layout* Sdesc, void* Y,
@@ -1083,12 +1081,10 @@ int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const 
   const int st = mx_args(Y, Ydesc, Qdesc->rows, Qdesc->cols, Q, Qdesc, S, Sdesc, a);
   if (st != QG_OK) return st;
   if (Qdesc->rows == 0 || Qdesc->cols == 0) return QG_OK;
-  a.Y = Y;
   a.cpr = (int32_t)cdiv(Qdesc->cols, 8);
-  a.units = Qdesc->rows * a.cpr;
-  if (mx_quant_blocks(a.units, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (mx_quant_blocks(Qdesc->rows * a.cpr, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (!h->online) return QG_ERR_HIP;
-  return launch_mx_dequantize(a, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+  return launch_mx_dequantize(a, Ydesc->type, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_plan(qg_handle* h, const qg_operation* op, const qg_layout* Adesc, const qg_layout* Udesc,

@@ -166,13 +166,13 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const MxQuantArgs
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const uint32_t off = i * kThreads + threadIdx.x;
-    live[i] = first + off < a.units;  // the same for a whole quad: units come in fours
+    live[i] = first + off < (int64_t)a.R * a.cpr;  // the same for a whole quad: units come in fours
     at[i] = places.at(off);
     int64_t src = at[i].row;
     if (a.rows && live[i]) src = a.rows[at[i].row];
     const int k = at[i].unit * 8;
     const int n = live[i] && src >= 0 && src < a.T ? a.K - k : 0;
-    const char* p = (const char*)a.X + (src * a.ldx + k) * Raw<DT>::ES;
+    const char* p = (const char*)a.X + (src * (int64_t)a.ldx + k) * Raw<DT>::ES;
     x[i].template load<true>(p, n);
     if constexpr (GATED) up[i].template load<false>(p + (int64_t)a.K * Raw<DT>::ES, n);
   }
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const uint32_t off = i * kThreads + threadIdx.x;
-    live[i] = first + off < a.units;
+    live[i] = first + off < (int64_t)a.R * a.cpr;
     at[i] = places.at(off);
     q[i] = s[i] = 0;
     if (live[i]) {
@@ -254,7 +254,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
     const int k = at[i].unit * 8;
     const int64_t base = at[i].row * a.ldx + k;
     if constexpr (DT == DT_F32) {
-      float* y = (float*)a.Y + base;
+      float* y = (float*)a.X + base;
       if (k + 8 <= a.K) {
         // two accesses that each fill half of every line: merged in the L2
         ((f32x4*)y)[0] = f32x4{v[0], v[1], v[2], v[3]};
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
           if (k + j < a.K) y[j] = v[j];
       }
     } else {
-      uint16_t* y = (uint16_t*)a.Y + base;
+      uint16_t* y = (uint16_t*)a.X + base;
       uint32_t h[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = DT == DT_BF16 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
@@ -282,23 +282,23 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
 
 template <int DT, bool GATED, int U>
 hipError_t quantize_u(const MxQuantArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx_quantize_kernel<DT, GATED, U>), dim3((unsigned)mx_quant_blocks(a.units, U)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((mx_quantize_kernel<DT, GATED, U>), dim3((unsigned)mx_quant_blocks((int64_t)a.R * a.cpr, U)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 // Several units per lane, for more loads in flight, once that still leaves
 // every CU eight workgroups; one below, so that few rows spread wide. 4096 rows
 // gathered to 32768 x 7168 and back: 178 us with four units both ways, 183 with
 // two, 209 with one; 8192 x 14336 gated and back: 149 us with two, 151 to 155 with one.
-bool several(const MxQuantArgs& a, int cus, int per_lane) { return a.units >= (int64_t)cus * 8 * per_lane * kThreads; }
+bool several(const MxQuantArgs& a, int cus, int per_lane) { return (int64_t)a.R * a.cpr >= (int64_t)cus * 8 * per_lane * kThreads; }
 
 template <int DT>
-hipError_t quantize_t(const MxQuantArgs& a, int cus, hipStream_t s) {
-  if (a.swiglu) return several(a, cus, 2) ? quantize_u<DT, true, 2>(a, s) : quantize_u<DT, true, 1>(a, s);
+hipError_t quantize_t(const MxQuantArgs& a, bool swiglu, int cus, hipStream_t s) {
+  if (swiglu) return several(a, cus, 2) ? quantize_u<DT, true, 2>(a, s) : quantize_u<DT, true, 1>(a, s);
   return several(a, cus, 4) ? quantize_u<DT, false, 4>(a, s) : quantize_u<DT, false, 1>(a, s);
 }
 template <int DT, int U>
 hipError_t dequantize_u(const MxQuantArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx_dequantize_kernel<DT, U>), dim3((unsigned)mx_quant_blocks(a.units, U)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((mx_dequantize_kernel<DT, U>), dim3((unsigned)mx_quant_blocks((int64_t)a.R * a.cpr, U)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 template <int DT>
@@ -310,17 +310,17 @@ hipError_t dequantize_t(const MxQuantArgs& a, int cus, hipStream_t s) {
 
 int64_t mx_quant_blocks(int64_t units, int per_lane) { return (units + kThreads * per_lane - 1) / (kThreads * per_lane); }
 
-hipError_t launch_mx_quantize(const MxQuantArgs& a, int cus, hipStream_t s) {
-  switch (a.x_type) {
-    case DT_F32: return quantize_t<DT_F32>(a, cus, s);
-    case DT_F16: return quantize_t<DT_F16>(a, cus, s);
-    case DT_BF16: return quantize_t<DT_BF16>(a, cus, s);
+hipError_t launch_mx_quantize(const MxQuantArgs& a, int x_type, bool swiglu, int cus, hipStream_t s) {
+  switch (x_type) {
+    case DT_F32: return quantize_t<DT_F32>(a, swiglu, cus, s);
+    case DT_F16: return quantize_t<DT_F16>(a, swiglu, cus, s);
+    case DT_BF16: return quantize_t<DT_BF16>(a, swiglu, cus, s);
     default: return hipErrorInvalidValue;
   }
 }
 
-hipError_t launch_mx_dequantize(const MxQuantArgs& a, int cus, hipStream_t s) {
-  switch (a.x_type) {
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, int x_type, int cus, hipStream_t s) {
+  switch (x_type) {
     case DT_F32: return dequantize_t<DT_F32>(a, cus, s);
     case DT_F16: return dequantize_t<DT_F16>(a, cus, s);
     case DT_BF16: return dequantize_t<DT_BF16>(a, cus, s);
