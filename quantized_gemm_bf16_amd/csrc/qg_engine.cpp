@@ -514,7 +514,11 @@ int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_wo
     a.tiles_m = (int32_t)(cdiv(p.M, k.bm) + p.E);  // upper bound on the padded m-tiles
     const int64_t ub = (int64_t)a.tiles_m * a.tiles_n;
     pl.tiles = (int)std::min<int64_t>(ub, INT32_MAX);
-    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ub, (int64_t)h->cus * 2));
+    // two workgroups per CU; three of the MXFP4 skinny kernel with a shared A,
+    // whose LDS lets them be resident (128 experts, 95 rows, N 5120, K 468: 37 us, 50
+    // with two of a deeper ring)
+    const int per_cu = k.family == FAM_MX_SKINNY && k.bn == 64 ? 3 : 2;
+    pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ub, (int64_t)h->cus * per_cu));
     pl.c.split = 1;
     pl.c.programs = 0;
   } else {
