@@ -28,6 +28,8 @@
 // does not hold, the wave redoes its units in 64 bits.
 #include "qg_mx_quant.hpp"
 
+#include <algorithm>
+
 #include "qg_args.hpp"
 #include "qg_device.hpp"
 
@@ -280,10 +282,32 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
   }
 }
 
+// A dispatch counts its threads in 32 bits, and a launch of more loses the rest without an error: rows go
+// out in parts of fewer (a row always fits).
+template <class Kernel>
+hipError_t launch_parts(Kernel kernel, const MxQuantArgs& a, int per_lane, int64_t value_pitch, hipStream_t s) {
+  const int64_t most = (int64_t)(UINT32_MAX / kThreads) * kThreads * per_lane / a.cpr;
+  for (int64_t r = 0; r < a.R; r += most) {
+    MxQuantArgs p = a;
+    p.R = (int32_t)std::min<int64_t>(most, a.R - r);
+    p.Q = a.Q + r * a.ldq;
+    p.S = a.S + r * a.lds;
+    if (a.rows) {
+      p.rows = a.rows + r;
+    } else {
+      p.X = (char*)a.X + r * value_pitch;
+      p.T = p.R;
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)mx_quant_blocks((int64_t)p.R * a.cpr, per_lane)), dim3(kThreads), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <int DT, bool GATED, int U>
 hipError_t quantize_u(const MxQuantArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx_quantize_kernel<DT, GATED, U>), dim3((unsigned)mx_quant_blocks((int64_t)a.R * a.cpr, U)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+  return launch_parts(mx_quantize_kernel<DT, GATED, U>, a, U, (int64_t)a.ldx * Raw<DT>::ES, s);
 }
 // Several units per lane, for more loads in flight, once that still leaves
 // every CU eight workgroups; one below, so that few rows spread wide. 4096 rows
@@ -298,8 +322,7 @@ hipError_t quantize_t(const MxQuantArgs& a, bool swiglu, int cus, hipStream_t s)
 }
 template <int DT, int U>
 hipError_t dequantize_u(const MxQuantArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx_dequantize_kernel<DT, U>), dim3((unsigned)mx_quant_blocks((int64_t)a.R * a.cpr, U)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
+  return launch_parts(mx_dequantize_kernel<DT, U>, a, U, (int64_t)a.ldx * Raw<DT>::ES, s);
 }
 template <int DT>
 hipError_t dequantize_t(const MxQuantArgs& a, int cus, hipStream_t s) {

@@ -238,3 +238,27 @@ def test_more_units_than_32_bits_count(g):
             assert bool(((a == b) | ((a | b) & (nibble & 119) == 0)).all())
     del q, s, y
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("act,n", [(qg.MX_SWIGLU, (1 << 16) + 5), (qg.MX_IDENTITY, (1 << 17) + 5)])
+def test_more_threads_than_one_launch_holds(g, act, n):
+    """A grid of 2^32 threads and more (two units to a thread gated, four plain): rows of 2^20, gathered from 3; every
+    byte of the codes and scales."""
+    k, t = 1 << 20, 3
+    x = sample(t, k * (1 + act), "bf16", 6)
+    xd = pitched(x, "bf16")
+    rows = torch.randint(0, t, (n,), device="cuda", dtype=torch.int32)
+    q = torch.full((n, k // 2), 0x5A, dtype=torch.uint8, device="cuda")
+    s = torch.full((n, k // 32), 0x5A, dtype=torch.uint8, device="cuda")
+    g.mx_quantize(xd, qg.layout("bf16", t, k * (1 + act)), q, qg.layout("e2m1", n, k), s, qg.layout("e8m0", n, k // 32), act=act,
+                  rows=rows)
+    few = quantise(g, xd, "bf16", k, act=act)
+    check(few, mx_ref.swiglu(x) if act else x)
+    code, byte = torch.from_numpy(mx_ref.pack(few[0])).cuda(), torch.from_numpy(few[1]).cuda()
+    step = 1 << 12
+    for i in range(0, n, step):
+        r = rows[i:i + step].long()
+        assert torch.equal(s[i:i + step], byte[r]), i
+        assert torch.equal(q[i:i + step], code[r]), i
+    del q, s
+    torch.cuda.empty_cache()
