@@ -526,8 +526,10 @@ int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_wo
     const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
     if (tiles > INT32_MAX / 64) return QG_ERR_UNSUPPORTED;
     pl.tiles = (int)tiles;
+    // a dispatch counts its threads in 32 bits; the kernels go round what does not fit
+    const auto blocks = [&](int64_t units) { return (int)std::min<int64_t>(units, UINT32_MAX / k.threads); };
     if (mode == MODE_DP) {
-      pl.grid = (int)tiles;
+      pl.grid = blocks(tiles);
       pl.c.split = 1;
       pl.c.programs = 0;
     } else if (mode == MODE_SPLITK) {
@@ -537,14 +539,14 @@ int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_wo
       a.splits = s;
       a.iters_per_split = ips;
       pl.c.split = s;
-      pl.grid = (int)(tiles * s);
+      pl.grid = blocks(tiles * s);
       pl.partials = (size_t)tiles * s * k.slot_bytes;
       pl.barriers = (size_t)tiles * 4;
       if (s == 1) {
         mode = MODE_DP;
         a.mode = pl.c.mode = MODE_DP;
         pl.partials = pl.barriers = 0;
-        pl.grid = (int)tiles;
+        pl.grid = blocks(tiles);
       }
     } else if (mode == MODE_STREAMK) {
       const int P = c.programs > 0 ? c.programs : h->cus;

@@ -286,3 +286,19 @@ def test_long_rows_past_32_bit_offsets(g, ws):
         buf[i * (stride // 2):i * (stride // 2) + n * k // 2] = p.b[i * n:(i + 1) * n].reshape(-1)
     p.b, p.bd = buf, qg.layout("e2m1", n, k, num=e, stride=stride)
     check(p, p.run(g, ws))
+
+
+@pytest.mark.parametrize("n", [1 << 28, (1 << 28) + 64])
+def test_columns_past_2_to_the_32_threads(g, ws, n):
+    """A row against 2^28 columns and more, each of 32 times 1, some of 32 times -2."""
+    q = torch.full((1, 16), 0x22, dtype=torch.uint8, device="cuda")
+    s = torch.full((1, 16), 127, dtype=torch.uint8, device="cuda")
+    bq = torch.full((n, 16), 0x22, dtype=torch.uint8, device="cuda")
+    bq[5::1001] = 0xCC
+    bs = torch.full((n, 16), 127, dtype=torch.uint8, device="cuda")
+    d = torch.full((1, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    g.run(qg.operation(quant_a=MX, quant_b=MX), 1.0, q, qg.layout("e2m1", 1, 32), s, qg.layout("e8m0", 1, 1), bq,
+          qg.layout("e2m1", n, 32), bs, qg.layout("e8m0", n, 1), 0.0, None, None, d, qg.layout("bf16", 1, n), ws.desc)
+    want = torch.full((1, n), 32.0, dtype=torch.bfloat16, device="cuda")
+    want[0, 5::1001] = -64.0
+    assert torch.equal(d, want)

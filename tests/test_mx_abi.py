@@ -203,3 +203,13 @@ def test_product_every_kernel_and_schedule_plans(g):
 def test_empty_product(g):
     assert run(g, operands(m=0)) == qg.OK
     assert ctypes.sizeof(qg.Layout) == 56
+
+
+def test_no_launch_of_2_to_the_32_threads(g):
+    """A dispatch counts its threads in 32 bits: 2^28 columns of a row are 2^24 tiles of 256 threads."""
+    ws = qg.Workspace(FAKE, qg.barriers_size(), FAKE, qg.partials_size())
+    for n in ((1 << 28) - 16, 1 << 28, (1 << 28) + 64):
+        p = plan(g, operands(1, n, 32), ws=ws)
+        assert "schedule=dp" in p and "_w4_" in p, p  # four waves
+        f = dict(x.split("=") for x in p.split())
+        assert int(f["tiles"]) == n // 16 and int(f["grid"]) * 256 < 1 << 32, p
