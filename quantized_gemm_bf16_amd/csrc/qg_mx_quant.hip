@@ -20,12 +20,15 @@
 //
 // SwiGLU: the codes are those of silu(g) * u without rounding before them, so
 // fp32 arithmetic alone would put values next to a rounding border on its
-// wrong side (about one in 10^6). The fp32 value v is within 2^-18 of the
-// exact one (for g >= -32: the argument of exp2 is off by at most 48 * 2^-24,
-// the other steps by a few 2^-23). Each lane rounds v (1 - 2^-17) and v (1 + 2^-17)
+// wrong side (about one in 10^6). The fp32 value v = (g u) rcp(1 + e), where
+// it is normal, is within 2^-18 of the exact one (for g >= -32: the argument of
+// exp2 is off by at most 48 * 2^-24, the other steps by a few 2^-23; g u, no
+// smaller than v, is normal too, where g rcp(1 + e) need not be). Each lane
+// rounds v (1 - 2^-17) and v (1 + 2^-17)
 // instead of v: equal codes are the exact value's code. Where they differ, or
 // the block maximum is as near a power of two, or fp32's range or the bound
-// does not hold, the wave redoes its units in 64 bits.
+// does not hold, the wave redoes its units in 64 bits. (A v below fp32's normal
+// range is a zero code in any block that is not redone: those reach 2^-60.)
 #include "qg_mx_quant.hpp"
 
 #include <algorithm>
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const MxQuantArgs
       if constexpr (GATED) {
         low = fminf(low, v[j]);
         const float e = __builtin_amdgcn_exp2f(v[j] * -1.44269504f);
-        v[j] = v[j] * __builtin_amdgcn_rcpf(1.f + e) * up[i].at(j);
+        v[j] = v[j] * up[i].at(j) * __builtin_amdgcn_rcpf(1.f + e);
       }
       top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7FFFFFFFu);
     }

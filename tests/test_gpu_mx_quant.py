@@ -262,3 +262,15 @@ def test_more_threads_than_one_launch_holds(g, act, n):
         assert torch.equal(q[i:i + step], code[r]), i
     del q, s
     torch.cuda.empty_cache()
+
+
+def test_swiglu_subnormal_gates(g):
+    """fp32 gates of a few bits against ups that bring the product far above fp32's smallest: g / (1 + exp(-g)) must not
+    be rounded to the subnormal grid on the way."""
+    r = np.random.default_rng(29)
+    n = 1024
+    at, by = r.integers(-149, -126, (n, 1)), r.integers(90, 121, (n, 1))
+    gate = np.ldexp(r.uniform(1, 8, (n, 32)) * r.choice([-1.0, 1.0], (n, 32)), at).astype(np.float32)
+    up = np.ldexp(r.uniform(1, 4, (n, 32)), by).astype(np.float32)
+    x = np.concatenate([gate, up], 1).astype(np.float64)
+    check(quantise(g, pitched(x, "f32"), "f32", 32, act=qg.MX_SWIGLU), mx_ref.swiglu(x), ignore_zero_sign=False)
