@@ -156,7 +156,8 @@ __device__ __attribute__((noinline)) uint64_t swiglu_codes64(Raw<DT> g, Raw<DT> 
     const double t = fabs(v[j]) * inv;
     // even codes take the ties: <= below them, < above
     const uint32_t c = (t > 0.25) + (t >= 0.75) + (t > 1.25) + (t >= 1.75) + (t > 2.5) + (t >= 3.5) + (t > 5.0);
-    q |= (c | (v[j] < 0 ? 8u : 0u)) << (4 * j);
+    // (the sign bit, as the 32-bit path has it: a -0 keeps its sign too)
+    q |= (c | (uint32_t)(__builtin_bit_cast(uint64_t, v[j]) >> 63) << 3) << (4 * j);
   }
   return q | (uint64_t)byte << 32;
 }

@@ -274,3 +274,19 @@ def test_swiglu_subnormal_gates(g):
     up = np.ldexp(r.uniform(1, 4, (n, 32)), by).astype(np.float32)
     x = np.concatenate([gate, up], 1).astype(np.float64)
     check(quantise(g, pitched(x, "f32"), "f32", 32, act=qg.MX_SWIGLU), mx_ref.swiglu(x), ignore_zero_sign=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_swiglu_bytes_do_not_depend_on_the_neighbours(g, dtype):
+    """A row's bytes, the sign of its zeros among them, are those of the row alone, whether or not other rows need 64 bits."""
+    k = 32
+    x = sample(64, 2 * k, dtype, 31, spread=1)
+    x[::2, 0:8] = 0.0
+    x[::2, 8:16] = -0.0
+    x[::4, k + 16:k + 24] = 0.0
+    x[1::2, 3] = -40.0
+    whole = quantise(g, pitched(x, dtype), dtype, k, act=qg.MX_SWIGLU)
+    check(whole, mx_ref.swiglu(x), ignore_zero_sign=False)
+    for i in range(0, 64, 2):
+        code, byte = quantise(g, pitched(x[i:i + 1], dtype), dtype, k, act=qg.MX_SWIGLU)
+        assert np.array_equal(code[0], whole[0][i]) and np.array_equal(byte[0], whole[1][i])
