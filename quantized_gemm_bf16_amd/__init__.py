@@ -251,7 +251,13 @@ class Gemm:
         return st, n.value
 
     def mx_quantize_raw(self, X, Xd, Q, Qd, S, Sd, act=MX_IDENTITY, rows=None, stream=None) -> int:
-        """qg_mx_quantize; returns the status code."""
+        """qg_mx_quantize; returns the status code. `rows`: a tensor (checked: int32, contiguous, an entry per row of Q at
+        least) or a raw device pointer."""
+        if rows is not None and not isinstance(rows, int):
+            if rows.dtype != torch.int32:
+                return ERR_UNSUPPORTED
+            if not rows.is_contiguous() or (Qd is not None and rows.numel() < Qd.rows):
+                return ERR_INVALID_ARG
         return lib.qg_mx_quantize(self.h, act, _ptr(X), Xd, _ptr(rows), _ptr(Q), Qd, _ptr(S), Sd,
                                   stream if stream is not None else _current_stream())
 

@@ -3,6 +3,7 @@ here reaches a launch (fake device addresses are never dereferenced)."""
 import ctypes
 
 import pytest
+import torch
 
 import quantized_gemm_bf16_amd as qg
 
@@ -213,3 +214,19 @@ def test_no_launch_of_2_to_the_32_threads(g):
         assert "schedule=dp" in p and "_w4_" in p, p  # four waves
         f = dict(x.split("=") for x in p.split())
         assert int(f["tiles"]) == n // 16 and int(f["grid"]) * 256 < 1 << 32, p
+
+
+def test_rows_tensor(g):
+    """What the binding can see of `rows`: entries of another size, apart from each other, or too few are refused."""
+    for t in (torch.int64, torch.int16, torch.uint8, torch.float32):
+        assert quant(g, rows=torch.zeros(8, dtype=t)) == qg.ERR_UNSUPPORTED, t
+    assert quant(g, rows=torch.zeros(4, 2, dtype=torch.int32)[:, 0]) == qg.ERR_INVALID_ARG
+    assert quant(g, rows=torch.zeros(3, dtype=torch.int32)) == qg.ERR_INVALID_ARG
+    assert quant(g, rows=torch.zeros(0, dtype=torch.int32)) == qg.ERR_INVALID_ARG
+    assert quant(g, rows=torch.zeros(4, dtype=torch.int32), qd=None) == qg.ERR_INVALID_ARG
+    with pytest.raises(qg.QGemmError) as e:
+        g.mx_quantize(FAKE, qg.layout("bf16", 4, 96), FAKE, qg.layout("e2m1", 4, 96), FAKE, qg.layout("e8m0", 4, 3),
+                      rows=torch.zeros(4, dtype=torch.int64))
+    assert e.value.status == qg.ERR_UNSUPPORTED
+    # an int32 tensor passes on: no rows of Q, nothing to do
+    assert quant(g, qd=qg.layout("e2m1", 0, 96), sd=qg.layout("e8m0", 0, 3), rows=torch.zeros(1, dtype=torch.int32)) == qg.OK
