@@ -265,9 +265,9 @@ typedef enum qg_mx_act {
  * of y without any rounding before them, the SwiGLU's too.
  *   X     f32 | bf16 | fp16, T x K (IDENTITY) or T x 2K (SWIGLU, gate columns
  *         first; K need not keep the second half aligned).
- *   rows  NULL (then T = rows of Q), or a DEVICE int32 array with one entry
- *         per row of Q: row i of Q comes from row rows[i] of X (a router's
- *         gather). An entry outside [0, T) gives a row of zeros.
+ *   rows  NULL (then T = rows of Q, or Q has none), or a DEVICE int32 array
+ *         with one entry per row of Q: row i of Q comes from row rows[i] of X
+ *         (a router's gather). An entry outside [0, T) gives a row of zeros.
  *   Q     QG_E2M1, rows x K; S QG_E8M0, rows x ceil(K/32): the operand and
  *         scale operand of qg_run as they are (of a grouped run too). Codes
  *         past K in the last block are written as zero; other padding is

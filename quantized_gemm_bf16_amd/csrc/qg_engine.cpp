@@ -1067,7 +1067,8 @@ int qg_mx_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc,
   if (!h || !Xdesc || !Qdesc || !Sdesc) return QG_ERR_INVALID_ARG;
   if (act != QG_MX_IDENTITY && act != QG_MX_SWIGLU) return QG_ERR_INVALID_ARG;
   MxQuantArgs a{};
-  const int64_t vrows = rows ? Xdesc->rows : Qdesc->rows;
+  // (an empty index array may have no address)
+  const int64_t vrows = rows || Qdesc->rows == 0 ? Xdesc->rows : Qdesc->rows;
   const int64_t vcols = act == QG_MX_SWIGLU ? 2 * Qdesc->cols : Qdesc->cols;
   const int st = mx_args(X, Xdesc, vrows, vcols, Q, Qdesc, S, Sdesc, a);
   if (st != QG_OK) return st;

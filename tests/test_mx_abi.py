@@ -230,3 +230,11 @@ def test_rows_tensor(g):
     assert e.value.status == qg.ERR_UNSUPPORTED
     # an int32 tensor passes on: no rows of Q, nothing to do
     assert quant(g, qd=qg.layout("e2m1", 0, 96), sd=qg.layout("e8m0", 0, 3), rows=torch.zeros(1, dtype=torch.int32)) == qg.OK
+
+
+def test_a_gather_of_no_rows(g):
+    """An empty index tensor has no address: with no rows of Q there is nothing to gather, however many rows X has."""
+    none = torch.zeros(0, dtype=torch.int32)
+    for act in (0, 1):
+        assert quant(g, act=act, q=None, s=None, n=0, xd=qg.layout("bf16", 7, 96 * (1 + act)), rows=none) == qg.OK
+    assert quant(g, xd=qg.layout("bf16", 7, 96)) == qg.ERR_INVALID_ARG  # with rows of Q they have to agree
