@@ -262,7 +262,8 @@ typedef enum qg_mx_act {
  * block gets too); an element becomes the E2M1 value nearest to it over the
  * scale, ties to the even code, magnitudes past 6 becoming 6. A block that
  * holds a NaN or an infinity gets the scale 255 and zero codes. The codes are those
- * of y without any rounding before them, the SwiGLU's too.
+ * of y without any rounding before them; the SwiGLU's are those of y as 64-bit
+ * arithmetic gives it, whatever the type of X.
  *   X     f32 | bf16 | fp16, T x K (IDENTITY) or T x 2K (SWIGLU, gate columns
  *         first; K need not keep the second half aligned).
  *   rows  NULL (then T = rows of Q, or Q has none), or a DEVICE int32 array

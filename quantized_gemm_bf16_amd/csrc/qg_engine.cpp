@@ -607,20 +607,22 @@ int skinny_for(const Problem& p, int64_t target_bn) {
 }
 
 // MXFP4. Few rows stream B: up to 16 rows of a plain product take the
-// k-interleaved skinny kernel (1 x 4096 x 14336: 9.2 us, 64 x 64 tiles 13.4), up
+// k-interleaved skinny kernel (1 x 4096 x 14336: 9.3 us, 64 x 64 tiles 13.4), up
 // to 32 its wider form while one workgroup per 16 columns fits on the CUs
-// (32 x 4096 x 14336: 11.8 against 13.4; N = 8192: 20 against 16.8), experts with
-// up to 4 rows on average the one that shares A (64 experts, 128 rows, N 2048,
-// K 7168: 85 us, 64 x 64 tiles 88, 128 x 128 tiles 98). Otherwise the tile with
+// (32 x 4096 x 14336: 11.8, 64 x 32 tiles 13.4; N = 8192: 20.2 against 14.6), experts
+// with up to 4 rows on average the one that shares A (64 experts, 128 rows, N 2048,
+// K 7168: 88 us, 64 x 64 tiles the same, 128 x 128 tiles 98; 128 experts, 95 rows,
+// N 5120, K 468: 38, 45 and 68). Otherwise the tile with
 // the least estimated time: a CU that has n tiles takes n (fixed + step per 256
 // of K), step being less for a tile that has the CU to itself. 64 x 32 tiles,
 // whose two groups of waves fill a CU, are for products of up to one tile per
-// CU. Measured, us, tiles of 64 x 32 / 64 / 128 / 256:
-//   64 x 8192 x 8192     11.2 / 13.8 /  20 /   -     333 x 1001 x 2075       7.9 / 8.2 /  13 /   -
-//   512 x 8192 x 8192      48 /   37 /  26 /  56     4096 x 4096 x 4096        - /  78 /  59 /  44
-//   64 experts, N 2048, K 7168: 1024 rows            - /  98 / 102 / 135     4096 rows   - / 138 / 130 / 139
-//                              16384 rows            - / 337 / 250 / 222
-//   8 experts, 16384 rows, N 4096, K 1000            - / 148 / 121 /  81
+// CU. Measured, us, tiles of 64 x 32 / 64 / 128 / 256 (twelve runs in a graph, the
+// start of the graph shared among them: up to 1 us over a run among others):
+//   64 x 8192 x 8192     11.2 / 13.9 /   - /   -     333 x 1001 x 2075       8.0 / 8.3 /  13 /   -
+//   512 x 8192 x 8192      66 /   38 /  26 /  57     4096 x 4096 x 4096      173 /  81 /  60 /  46
+//   64 experts, N 2048, K 7168: 1024 rows          138 /  98 / 102 / 129     4096 rows 217 / 137 / 131 / 141
+//                              16384 rows          652 / 336 / 249 / 221
+//   8 experts, 16384 rows, N 4096, K 1000          482 / 149 / 121 /  81
 Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, int forced_mode) {
   Choice c;
   const double cus = h->cus;
@@ -653,7 +655,7 @@ Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws
   }
   // A long K over few tiles: up to eight chunks that fit on the CUs together,
   // four k-tiles each at least, where they save more than the 4 us that the
-  // partial tiles cost (64 x 1024 x 14336: 10.9 us in eight chunks, 14 whole).
+  // partial tiles cost (64 x 1024 x 14336: 11.2 us in eight chunks, 14 whole).
   if (c.kernel < 0 || p.E > 0 || forced_mode >= 0 || !ws || !ws->partials || !ws->barriers) return c;
   const KernelInfo& k = kKernels[c.kernel];
   const int64_t tiles = cdiv(p.M, k.bm) * cdiv(p.N, k.bn), iters = cdiv(p.K, k.bk);

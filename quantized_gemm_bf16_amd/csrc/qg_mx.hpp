@@ -92,7 +92,7 @@ __device__ __forceinline__ int pinned_lane(int x) {
 // ---- tiles ------------------------------------------------------------------
 // The LDS ring, swizzle and epilogue of the tile core, with ROWB bytes (2 ROWB
 // codes) of each row per stage. Large products are bound by power: 4096^3
-// takes 42 us (3.27 PFLOP/s) at a shader clock of 1.8 GHz, of which an MFMA-only
+// takes 42 to 46 us (up to 3.27 PFLOP/s) at a shader clock of 1.8 GHz, of which an MFMA-only
 // copy of the loop takes 25 and a launch and the stores 8, and a grouped prompt
 // (64 experts, 65536 x 2048 x 7168) 660 us; small ones by the latency of
 // their few k-tiles. What the loop does about both:

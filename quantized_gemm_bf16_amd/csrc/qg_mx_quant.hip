@@ -13,10 +13,11 @@
 // nothing goes through LDS. Units are numbered row after row, whatever K is, so
 // that a wave is full at any width; a workgroup does one division to find its
 // first row and its lanes one multiplication each. Measured, bf16: 8192 x 14336
-// gated 100 us (532 MB, 5.3 TB/s; a copy of 1 GiB reaches 5.15), 4096 rows
-// gathered to 32768 x 7168 92 us (each row read eight times, mostly from the
-// caches), the same codes back to values 85 us (594 MB, 7 TB/s: the codes come
-// from the memory-side cache), one row of 4096 2 us each way.
+// gated 99 us (532 MB, 5.4 TB/s; a copy of 1 GiB reaches 5.15), 4096 rows
+// gathered to 32768 x 7168 91 us (each row read eight times, mostly from the
+// caches; its own 184 MB would take 36; gated 162), the same codes back to
+// values 84 us (594 MB, 7 TB/s: the codes come from the memory-side cache), one
+// row of 4096 2 us each way.
 //
 // SwiGLU: the codes are those of silu(g) * u without rounding before them, so
 // fp32 arithmetic alone would put values next to a rounding border on its
@@ -29,6 +30,9 @@
 // the block maximum is as near a power of two, or fp32's range or the bound
 // does not hold, the wave redoes its units in 64 bits. (A v below fp32's normal
 // range is a zero code in any block that is not redone: those reach 2^-60.)
+// Normal values ask for it so seldom that it does not show beside the memory;
+// with one gate in 10^4 below -32 (a wave in 20) 8192 x 14336 takes 106 us,
+// with one in 1000 175 and once every wave is redone 290.
 #include "qg_mx_quant.hpp"
 
 #include <algorithm>

@@ -18,7 +18,7 @@
 //
 // Measured: 1 x 4096 x 14336 k-interleaved in 8.3 us (31 MB: 3.8 TB/s with the
 // launch; the mainloops take 6.0), 64 experts of 2048 x 7168 with 128 rows
-// N-split in 84.7 us (477 MB: 5.6 TB/s, a plain streaming read 5.9). Four waves
+// N-split in 84 us (477 MB: 5.7 TB/s, a plain streaming read 5.9). Four waves
 // and two blocks each: eight waves 9.4 us, 32 columns per workgroup 9.7. The
 // shared ring takes two blocks too, so that three workgroups fit on a CU: with
 // three blocks and two workgroups the same at K = 7168, but 33 instead of 30 us
