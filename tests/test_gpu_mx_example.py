@@ -61,3 +61,31 @@ def test_expert_block(tokens, experts, top_k, hidden, inner):
     np.add.at(want, order // top_k, part)
     np.add.at(size, order // top_k, np.abs(part))
     assert (np.abs(y - want) <= 2.0 ** -24 * (top_k + 1) * size).all()
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,inner", [(1, 4, 2, 64, 32), (300, 16, 4, 512, 264)])
+def test_expert_block_in_a_graph(tokens, experts, top_k, hidden, inner):
+    """Captured, the block gives what it gives eagerly, replay after replay, with other tokens and other experts chosen."""
+    torch.manual_seed(7)
+
+    def inputs():
+        share, ids = torch.randn(tokens, experts, device="cuda").softmax(-1).topk(top_k, -1)
+        return torch.randn(tokens, hidden, device="cuda", dtype=torch.bfloat16), ids, share
+
+    w1 = torch.randn(experts, 2 * inner, hidden, device="cuda", dtype=torch.bfloat16) * 0.1
+    w2 = torch.randn(experts, hidden, inner, device="cuda", dtype=torch.bfloat16) * 0.1
+    block = example().ExpertBlock(qg.Gemm(), w1, w2, tokens, top_k)
+    held = inputs()
+    block(*held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block(*held)
+    for _ in range(4):
+        new = inputs()
+        want = block(*new).clone()
+        for t, n in zip(held, new):
+            t.copy_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
