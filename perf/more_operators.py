@@ -327,8 +327,8 @@ def run_own(st):
         engine.group_rows(case["experts"], st["ids"], st["id"], st["offsets"], st["rows"], st["back"], space.desc)
         return st["offsets"], st["rows"], st["back"]
     if op in ("quantise", "gated"):
-        engine.i8_quantize(st["x"], st["xd"], st["q"], st["qd"], st["s"], st["sd"], act=st["act"], rows=st.get("index"))
-        engine.i8_dequantize(st["q"], st["qd"], st["s"], st["sd"], st["y"], st["yd"])
+        engine.int_quantize(st["x"], st["xd"], st["q"], st["qd"], st["s"], st["sd"], act=st["act"], rows=st.get("index"))
+        engine.int_dequantize(st["q"], st["qd"], st["s"], st["sd"], st["y"], st["yd"])
         return st["y"][:, :case["k"]]
     if op == "product":
         engine.run(st["op"], 1.0, st["a"], st["ad"], st["u"], st["ud"], st["b"], st["bd"], st["v"], st["vd"],
