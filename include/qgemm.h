@@ -229,9 +229,10 @@ size_t qg_partials_size(void);
  *   A, B int8 -> D int32, C int32; alpha must be 1 and beta 0 or 1 (exact)
  *   A, B int8 + U, V fp32 (w8a8: QG_QUANT_BLOCK_F32 on both with group_mn = 1
  *     and group_k = 0 or >= K, i.e. one scale per row of A and per row of B;
- *     U is M x >=1, V is N x >=1, any ld >= 1, 4-byte aligned) -> the exact
- *     int32 sum times U[m] * V[n] in fp32, then the float epilogue; D f32 |
- *     bf16 | fp16 (or int8 codes), C f32 | bf16 | fp16; not grouped/batched
+ *     U is M x >=1, V is N x >=1, any ld >= 1, 4-byte aligned; grouped: V's
+ *     num and stride as B's) -> the exact int32 sum times U[m] * V[n] in fp32,
+ *     then the float epilogue; D f32 | bf16 | fp16 (or int8 codes), C f32 |
+ *     bf16 | fp16
  *   A, B e2m1 + U, V e8m0 (MXFP4: QG_QUANT_MX on both, group_k 32, group_mn
  *     1) -> D f32 | bf16 | fp16, C f32 | bf16 | fp16. A block whose scale is
  *     255 (NaN) makes the outputs that read it NaN. Codes past K, scales past
@@ -284,6 +285,72 @@ int qg_mx_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc,
  * and rules. */
 int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const void* S, const qg_layout* Sdesc, void* Y,
                      const qg_layout* Ydesc, hipStream_t stream);
+
+/* ---- int8 operands ------------------------------------------------------- */
+/* Quantises y = act(X) (qg_mx_act), rows x K, to int8 with one scale per row: S = amax / 127 rounded to fp32, amax
+ * being the row's largest magnitude; Q = y / S rounded to the nearest integer, ties to even (at most 127 in
+ * magnitude). Both are those of 64-bit arithmetic, y without any rounding before. A row of zeros has scale 0; a
+ * row that holds a NaN or an infinity, or whose scale would pass fp32's range, has scale NaN and zero codes.
+ *   X     f32 | bf16 | fp16, T x K (IDENTITY) or T x 2K (SWIGLU, gate columns first); K at most 65536.
+ *   rows  as in qg_mx_quantize: row i of Q comes from row rows[i] of X, or is zero (scale 0) where that is outside [0, T).
+ *   Q     QG_I8, rows x K; S QG_F32, rows x >= 1 (its first column): operand and scales of a w8a8 qg_run as they are,
+ *         A and U or B and V, grouped or not. Row padding is left alone.
+ * Pointers and pitches of X and Q must be multiples of 16 bytes (S, rows: 4). Asynchronous on `stream`, allocates nothing. */
+int qg_int_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc, const int32_t* rows, void* Q,
+                   const qg_layout* Qdesc, float* S, const qg_layout* Sdesc, hipStream_t stream);
+/* Y[i, k] = Q[i, k] * S[i], formed in fp32 or finer and rounded (RNE) to Y's type (f32 | bf16 | fp16); NaN where the scale
+ * is. Same layouts and rules. */
+int qg_int_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const float* S, const qg_layout* Sdesc, void* Y,
+                     const qg_layout* Ydesc, hipStream_t stream);
+
+/* ---- around an expert block's products ------------------------------------ */
+typedef enum qg_route_score {
+  QG_ROUTE_SOFTMAX = 0, /* p[t, e] = exp(x[t, e]) / sum over e of the same */
+  QG_ROUTE_SIGMOID = 1  /* p[t, e] = 1 / (1 + exp(-x[t, e])) */
+} qg_route_score;
+
+typedef struct qg_routing {
+  int32_t score;       /* qg_route_score */
+  int32_t top_k;       /* experts per token, 1 .. 32 */
+  int32_t groups;      /* equal groups of consecutive experts; 0 or 1: none */
+  int32_t top_groups;  /* groups a token may choose from (ignored without groups, like group_best) */
+  int32_t group_best;  /* 1: a group stands by its best key; 2: by the sum of its two best (of one, where it has one) */
+  int32_t renormalize; /* weights over the sum of the chosen ones' scores */
+  float scale;         /* times this */
+  int32_t reserved;
+} qg_routing;
+
+/* Chooses each token's experts from a router's logits X (T x E, f32 | bf16 | fp16).
+ * An expert's key is p + bias (bias: DEVICE, E fp32, for balance; it has no part in the weights), or the logit where
+ * bias is NULL (the order of the scores). The best `top_groups` groups keep their experts; of those the `top_k` best
+ * keys are chosen, best first. All comparisons are those of 64-bit arithmetic, ties go to the lowest index. Never
+ * chosen: an expert whose logit or key is NaN or -inf (a masked one; a group of such stands below all others). Where
+ * fewer than top_k are left, ids -1 with weight 0 fill the row (all of it, where everything is masked).
+ * In a softmax with logits of +inf these share the whole of it.
+ *   ids  QG_I32, T x top_k; W QG_F32, T x top_k: p, over the chosen ones' sum where `renormalize`, times `scale`.
+ * E is at most 1024, groups at most 64; with groups that are no power of two, experts per group times the next power of two
+ * is at most 1024. X's pointer and pitch must be multiples of 16 bytes, the others' of 4. Asynchronous on `stream`,
+ * allocates nothing. */
+int qg_route(qg_handle* h, const qg_routing* routing, const void* X, const qg_layout* Xdesc, const float* bias, int32_t* ids,
+             const qg_layout* Idesc, float* W, const qg_layout* Wdesc, hipStream_t stream);
+
+/* Sorts choices by expert (stable: within an expert in the order of tokens, then of choices).
+ *   ids      QG_I32, T x K; an entry outside [0, experts) belongs to nobody (masked, or another process holds that expert).
+ *   offsets  DEVICE, experts + 1: the `offsets` of a grouped qg_run over T * K rows.
+ *   rows     DEVICE, T * K: the token of each sorted row, the `rows` of a quantiser; -1 behind offsets[experts].
+ *   back     DEVICE, T * K: the sorted row of each choice, -1 for nobody's; qg_combine's `back`.
+ * experts is at most 1023, T * K at most 2^30. `ws` may be NULL for up to 8192 choices; beyond, 1024 bytes of its
+ * partials per expert are used. Asynchronous on `stream`, allocates nothing. */
+int qg_group_rows(qg_handle* h, int experts, const int32_t* ids, const qg_layout* Idesc, int32_t* offsets, int32_t* rows,
+                  int32_t* back, const qg_workspace* ws, hipStream_t stream);
+
+/* Y[t] = sum over k of W[t, k] * R[back[t, k]] + beta * C[t]: each token's rows of the experts' results, weighted, and
+ * what a shared expert (or the residual) gave. Sums are fp32, k in order, rounded once (RNE) to Y's type.
+ *   R     f32 | bf16 | fp16, N x H; back: DEVICE, T x K int32, contiguous; an entry outside [0, N) adds nothing.
+ *   W     QG_F32, T x K; C (read only when beta != 0) and Y f32 | bf16 | fp16, T x H, rows at multiples of 16 bytes.
+ *         Y may be C. Asynchronous on `stream`, allocates nothing. */
+int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_t* back, const float* W, const qg_layout* Wdesc,
+               float beta, const void* C, const qg_layout* Cdesc, void* Y, const qg_layout* Ydesc, hipStream_t stream);
 
 /* qg_run without a workspace argument, for callers that cannot allocate
  * device memory (code under HIP graph capture, tight serving loops, harnesses

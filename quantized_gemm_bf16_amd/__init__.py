@@ -29,6 +29,7 @@ POLICY_DEFAULT, POLICY_MEASURE, POLICY_REUSE, POLICY_FORCE = 0, 1, 2, 3
 EPI_ALPHA_BETA, EPI_BIAS, EPI_RELU, EPI_GELU, EPI_QUANT_I8 = 0, 1, 2, 4, 8
 QUANT_NONE, QUANT_INT4_ZP, QUANT_BLOCK_F32, QUANT_MX = 0, 1, 2, 3
 MX_IDENTITY, MX_SWIGLU = 0, 1
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
 SCHED_AUTO, SCHED_DP, SCHED_SPLITK, SCHED_STREAMK = 0, 1, 2, 3
 
 OK = 0
@@ -42,7 +43,8 @@ EXPORTS = ["qg_create", "qg_destroy", "qg_barriers_size", "qg_partials_size", "q
            "qg_export", "qg_import", "qg_get_tuning_seq", "qg_cache_size", "qg_kernel_count",
            "qg_kernel_name", "qg_status_str", "qg_version", "qg_streamk_units", "qg_streamk_fixup",
            "qg_run_noalloc", "qg_noalloc_barriers_size", "qg_noalloc_partials_size", "qg_run_timed",
-           "qg_mx_quantize", "qg_mx_dequantize"]
+           "qg_mx_quantize", "qg_mx_dequantize", "qg_int_quantize", "qg_int_dequantize", "qg_route",
+           "qg_group_rows", "qg_combine"]
 
 
 class Layout(ctypes.Structure):
@@ -72,6 +74,12 @@ class Workspace(ctypes.Structure):
                 ("partials", ctypes.c_void_p), ("partials_size", ctypes.c_size_t)]
 
 
+class Routing(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("top_k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class QGemmError(RuntimeError):
     def __init__(self, status, what=""):
         self.status = status
@@ -97,6 +105,11 @@ def _load(path=LIB_PATH):
                                vp, ctypes.c_int64, P(ctypes.c_int64)]
     L.qg_mx_quantize.argtypes = [vp, i32, vp, P(Layout), vp, vp, P(Layout), vp, P(Layout), vp]
     L.qg_mx_dequantize.argtypes = [vp, vp, P(Layout), vp, P(Layout), vp, P(Layout), vp]
+    L.qg_int_quantize.argtypes = [vp, i32, vp, P(Layout), vp, vp, P(Layout), vp, P(Layout), vp]
+    L.qg_int_dequantize.argtypes = [vp, vp, P(Layout), vp, P(Layout), vp, P(Layout), vp]
+    L.qg_route.argtypes = [vp, P(Routing), vp, P(Layout), vp, vp, P(Layout), vp, P(Layout), vp]
+    L.qg_group_rows.argtypes = [vp, i32, vp, P(Layout), vp, vp, vp, P(Workspace), vp]
+    L.qg_combine.argtypes = [vp, vp, P(Layout), vp, vp, P(Layout), ctypes.c_float, vp, P(Layout), vp, P(Layout), vp]
     L.qg_noalloc_barriers_size.restype = sz
     L.qg_noalloc_partials_size.restype = sz
     L.qg_plan.argtypes = [vp, P(Operation), P(Layout), P(Layout), P(Layout), P(Layout), P(Layout), P(Layout),
@@ -116,7 +129,8 @@ def _load(path=LIB_PATH):
     for name in ("qg_create", "qg_destroy", "qg_run", "qg_run_noalloc", "qg_run_timed", "qg_plan", "qg_export",
                  "qg_import",
                  "qg_get_tuning_seq", "qg_cache_size", "qg_streamk_units", "qg_streamk_fixup",
-                 "qg_mx_quantize", "qg_mx_dequantize"):
+                 "qg_mx_quantize", "qg_mx_dequantize", "qg_int_quantize", "qg_int_dequantize", "qg_route",
+                 "qg_group_rows", "qg_combine"):
         getattr(L, name).restype = i32
     return L
 
@@ -190,6 +204,26 @@ def operation(policy=POLICY_DEFAULT, schedule=SCHED_AUTO, split_k=0, programs=0,
     epi = EpilogueArgs(_ptr(bias), bt, 0, _ptr(row_scale), float(zero_point), 0)
     return Operation(policy, int(epilogue), Quant(*quant_a), Quant(*quant_b), schedule, split_k, programs, kernel,
                      epi)
+
+
+def routing(score=ROUTE_SOFTMAX, top_k=1, groups=1, top_groups=1, group_best=1, renormalize=False,
+            scale=1.0) -> Routing:
+    return Routing(int(score), int(top_k), int(groups), int(top_groups), int(group_best), int(bool(renormalize)),
+                   float(scale), 0)
+
+
+def _bad_table(t, dtype, n=0):
+    """A status where `t` is a tensor that is not what a call without a layout for it reads: `dtype`, contiguous, n
+    elements at least (raw pointers and None are the caller's word)."""
+    if t is None or isinstance(t, int):
+        return OK
+    if t.dtype != dtype:
+        return ERR_UNSUPPORTED
+    return OK if t.is_contiguous() and t.numel() >= n else ERR_INVALID_ARG
+
+
+def _bad_type(t, dtype):
+    return ERR_UNSUPPORTED if not (t is None or isinstance(t, int)) and t.dtype != dtype else OK
 
 
 def _ptr(t):
@@ -274,6 +308,71 @@ class Gemm:
     def mx_dequantize(self, Q, Qd, S, Sd, Y, Yd, stream=None):
         """MXFP4 codes Q and scales S to the values Y that they stand for."""
         _check(self.mx_dequantize_raw(Q, Qd, S, Sd, Y, Yd, stream), "qg_mx_dequantize")
+
+    def int_quantize_raw(self, X, Xd, Q, Qd, S, Sd, act=MX_IDENTITY, rows=None, stream=None) -> int:
+        """qg_int_quantize; returns the status code. `rows` as in mx_quantize_raw."""
+        st = _bad_table(rows, torch.int32, Qd.rows if Qd is not None else 0) or _bad_type(S, torch.float32)
+        if st:
+            return st
+        return lib.qg_int_quantize(self.h, act, _ptr(X), Xd, _ptr(rows), _ptr(Q), Qd, _ptr(S), Sd,
+                                  stream if stream is not None else _current_stream())
+
+    def int_quantize(self, X, Xd, Q, Qd, S, Sd, act=MX_IDENTITY, rows=None, stream=None):
+        """Rows of X (all, or those that the device int32 array `rows` names) to int8 codes Q and fp32 scales S, a
+        scale per row, through `act` (MX_IDENTITY, MX_SWIGLU)."""
+        _check(self.int_quantize_raw(X, Xd, Q, Qd, S, Sd, act, rows, stream), "qg_int_quantize")
+
+    def int_dequantize_raw(self, Q, Qd, S, Sd, Y, Yd, stream=None) -> int:
+        """qg_int_dequantize; returns the status code."""
+        return _bad_type(S, torch.float32) or lib.qg_int_dequantize(
+            self.h, _ptr(Q), Qd, _ptr(S), Sd, _ptr(Y), Yd, stream if stream is not None else _current_stream())
+
+    def int_dequantize(self, Q, Qd, S, Sd, Y, Yd, stream=None):
+        """int8 codes Q and scales S to the values Y that they stand for."""
+        _check(self.int_dequantize_raw(Q, Qd, S, Sd, Y, Yd, stream), "qg_int_dequantize")
+
+    def route_raw(self, routing, X, Xd, bias, ids, Id, W, Wd, stream=None) -> int:
+        """qg_route; returns the status code. `bias`: a contiguous fp32 tensor with an entry per expert, None, or a raw
+        device pointer."""
+        st = (_bad_table(bias, torch.float32, Xd.cols if Xd is not None else 0) or _bad_type(ids, torch.int32)
+              or _bad_type(W, torch.float32))
+        if st:
+            return st
+        return lib.qg_route(self.h, routing, _ptr(X), Xd, _ptr(bias), _ptr(ids), Id, _ptr(W), Wd,
+                            stream if stream is not None else _current_stream())
+
+    def route(self, routing, X, Xd, bias, ids, Id, W, Wd, stream=None):
+        """Each token's experts `ids` and their weights W from the logits X, by `routing` (see routing())."""
+        _check(self.route_raw(routing, X, Xd, bias, ids, Id, W, Wd, stream), "qg_route")
+
+    def group_rows_raw(self, experts, ids, Id, offsets, rows, back, ws=None, stream=None) -> int:
+        """qg_group_rows; returns the status code. offsets, rows, back: contiguous int32 tensors of experts + 1 and
+        (an entry per choice) entries, or raw device pointers."""
+        n = Id.rows * Id.cols if Id is not None else 0
+        st = (_bad_type(ids, torch.int32) or _bad_table(offsets, torch.int32, experts + 1)
+              or _bad_table(rows, torch.int32, n) or _bad_table(back, torch.int32, n))
+        if st:
+            return st
+        return lib.qg_group_rows(self.h, experts, _ptr(ids), Id, _ptr(offsets), _ptr(rows), _ptr(back), ws,
+                                 stream if stream is not None else _current_stream())
+
+    def group_rows(self, experts, ids, Id, offsets, rows, back, ws=None, stream=None):
+        """Choices `ids` sorted by expert: offsets of the experts' runs, source row of each sorted row, and where each
+        choice went."""
+        _check(self.group_rows_raw(experts, ids, Id, offsets, rows, back, ws, stream), "qg_group_rows")
+
+    def combine_raw(self, R, Rd, back, W, Wd, Y, Yd, beta=0.0, C=None, Cd=None, stream=None) -> int:
+        """qg_combine; returns the status code. `back`: a contiguous int32 tensor, or a raw device pointer."""
+        st = (_bad_table(back, torch.int32, Wd.rows * Wd.cols if Wd is not None else 0)
+              or _bad_type(W, torch.float32))
+        if st:
+            return st
+        return lib.qg_combine(self.h, _ptr(R), Rd, _ptr(back), _ptr(W), Wd, float(beta), _ptr(C), Cd, _ptr(Y), Yd,
+                              stream if stream is not None else _current_stream())
+
+    def combine(self, R, Rd, back, W, Wd, Y, Yd, beta=0.0, C=None, Cd=None, stream=None):
+        """Y[t] = sum_k W[t, k] R[back[t, k]] + beta C[t]."""
+        _check(self.combine_raw(R, Rd, back, W, Wd, Y, Yd, beta, C, Cd, stream), "qg_combine")
 
     def plan(self, op, Ad, Ud, Bd, Vd, Cd, Dd, alpha, beta, ws=None) -> str:
         buf = ctypes.create_string_buffer(512)

@@ -23,6 +23,8 @@
 
 #include "../../include/qgemm.h"
 #include "qg_args.hpp"
+#include "qg_experts.hpp"
+#include "qg_i8_quant.hpp"
 #include "qg_mx_quant.hpp"
 #include "qg_registry.hpp"
 #include "qg_streamk.hpp"
@@ -246,7 +248,6 @@ int validate(const qg_operation* op, float alpha, const void* A, const qg_layout
     const qg_quant &qa = op->quant_a, &qb = op->quant_b;
     if (qa.group_mn != 1 || qb.group_mn != 1) return QG_ERR_UNSUPPORTED;
     if ((qa.group_k != 0 && qa.group_k < p.K) || (qb.group_k != 0 && qb.group_k < p.K)) return QG_ERR_UNSUPPORTED;
-    if (grouped) return QG_ERR_UNSUPPORTED;
     if (!Ud || !Vd) return QG_ERR_INVALID_ARG;
     if ((st = check_layout(Ud)) || (st = check_layout(Vd))) return st;
     if (Ud->type != QG_F32 || Vd->type != QG_F32) return QG_ERR_UNSUPPORTED;
@@ -254,6 +255,13 @@ int validate(const qg_operation* op, float alpha, const void* A, const qg_layout
       return QG_ERR_INVALID_ARG;
     if (p.M > 0 && p.N > 0 && (!U || !V)) return QG_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(U) & 3) || (reinterpret_cast<uintptr_t>(V) & 3)) return QG_ERR_ALIGNMENT;
+    if (grouped) {
+      if (Vd->num != Ad->num) return QG_ERR_INVALID_ARG;
+      if (Ud->offsets && Ud->offsets != Ad->offsets) return QG_ERR_UNSUPPORTED;
+      p.v_batch = Vd->stride;
+      if (p.v_batch != 0 && p.v_batch < Vd->rows * Vd->ld) return QG_ERR_INVALID_ARG;
+      if (!Ad->offsets && (Ud->num != Ad->num || Ud->stride != Ud->rows * Ud->ld)) return QG_ERR_UNSUPPORTED;
+    }
     if (!(p.td == QG_F32 || p.td == QG_BF16 || p.td == QG_F16 || p.td == QG_I8)) return QG_ERR_UNSUPPORTED;
     p.w8a8 = true;
     p.U = U;
@@ -433,6 +441,83 @@ int mx_args(const void* vals, const qg_layout* Vd, int64_t vrows, int64_t vcols,
   a.T = (int32_t)vrows;
   a.Q = (char*)const_cast<void*>(Q);
   a.S = (char*)const_cast<void*>(S);
+  return QG_OK;
+}
+
+// ---- int8 quantise / dequantise, and the operators around an expert block's products ----
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+bool is_float(int t) { return t == QG_F32 || t == QG_BF16 || t == QG_F16; }
+
+// rows x cols of one type; a row begins on 16 bytes, or (`loose`: small int32 and fp32 tables) anywhere.
+int check_table(const void* ptr, const qg_layout* L, int64_t rows, int64_t cols, bool loose = false) {
+  if (L->rows != rows || L->cols != cols || L->ld < cols) return QG_ERR_INVALID_ARG;
+  if (L->num > 1 && !L->offsets) return QG_ERR_UNSUPPORTED;  // batched
+  if (rows > 0 && cols > 0 && !ptr) return QG_ERR_INVALID_ARG;
+  if (loose ? !aligned4(ptr) : row_bytes(L->type, L->ld) % 16 || !aligned16(ptr)) return QG_ERR_ALIGNMENT;
+  return QG_OK;
+}
+
+int i8_args(const void* vals, const qg_layout* Vd, int64_t vrows, int64_t vcols, const void* Q, const qg_layout* Qd,
+            const void* S, const qg_layout* Sd, I8QuantArgs& a) {
+  int st;
+  if ((st = check_layout(Vd)) || (st = check_layout(Qd)) || (st = check_layout(Sd))) return st;
+  if (!is_float(Vd->type) || Qd->type != QG_I8 || Sd->type != QG_F32) return QG_ERR_UNSUPPORTED;
+  if (Sd->cols < 1 || Sd->ld < 1) return QG_ERR_INVALID_ARG;
+  if ((st = check_table(Q, Qd, Qd->rows, Qd->cols))) return st;
+  if (Sd->rows != Qd->rows || (Qd->rows > 0 && !S)) return QG_ERR_INVALID_ARG;
+  if (Sd->num > 1 && !Sd->offsets) return QG_ERR_UNSUPPORTED;
+  if (!aligned4(S)) return QG_ERR_ALIGNMENT;
+  if ((st = check_table(vals, Vd, vrows, vcols))) return st;
+  a.X = const_cast<void*>(vals);
+  a.Q = (char*)const_cast<void*>(Q);
+  a.S = (float*)const_cast<void*>(S);
+  a.ldx = (int32_t)Vd->ld;
+  a.ldq = (int32_t)Qd->ld;
+  a.lds = (int32_t)Sd->ld;
+  a.T = (int32_t)vrows;
+  a.K = (int32_t)Qd->cols;
+  a.R = (int32_t)Qd->rows;
+  a.cpr = (int32_t)cdiv(Qd->cols, 8);
+  return QG_OK;
+}
+
+int route_args(const qg_routing* r, const void* X, const qg_layout* Xd, const float* bias, int32_t* ids,
+               const qg_layout* Id, float* W, const qg_layout* Wd, RouteArgs& a) {
+  int st;
+  if ((st = check_layout(Xd)) || (st = check_layout(Id)) || (st = check_layout(Wd))) return st;
+  if (!is_float(Xd->type) || Id->type != QG_I32 || Wd->type != QG_F32) return QG_ERR_UNSUPPORTED;
+  if (r->score != QG_ROUTE_SOFTMAX && r->score != QG_ROUTE_SIGMOID) return QG_ERR_INVALID_ARG;
+  const int64_t E = Xd->cols;
+  if (E < 1 || r->top_k < 1 || r->groups < 0 || !std::isfinite(r->scale)) return QG_ERR_INVALID_ARG;
+  const int groups = std::max(1, r->groups), kept = groups > 1 ? r->top_groups : 1;
+  if (E % groups || kept < 1 || kept > groups) return QG_ERR_INVALID_ARG;
+  if (groups > 1 && r->group_best != 1 && r->group_best != 2) return QG_ERR_INVALID_ARG;
+  const int64_t per = E / groups;
+  if (r->top_k > kept * per) return QG_ERR_INVALID_ARG;
+  if (r->top_k > kRouteMaxK || groups > kRouteMaxGroups) return QG_ERR_UNSUPPORTED;
+  // a group takes an aligned power of two of the wave's lanes, up to 16 experts each
+  int shift = 6;
+  while ((groups << shift) > 64) --shift;
+  if (per > (int64_t)(kRouteMaxExperts / 64) << shift) return QG_ERR_UNSUPPORTED;
+  if ((st = check_table(X, Xd, Xd->rows, E))) return st;
+  if ((st = check_table(ids, Id, Xd->rows, r->top_k, true)) || (st = check_table(W, Wd, Xd->rows, r->top_k, true))) return st;
+  if (!aligned4(bias)) return QG_ERR_ALIGNMENT;
+  a.X = X;
+  a.bias = bias;
+  a.ids = ids;
+  a.W = W;
+  a.T = Xd->rows;
+  a.ldx = (int32_t)Xd->ld;
+  a.ldi = (int32_t)Id->ld;
+  a.ldw = (int32_t)Wd->ld;
+  a.K = r->top_k;
+  a.groups = groups;
+  a.per = (int32_t)per;
+  a.kept = kept;
+  a.shift = shift;
+  a.flags = (r->score == QG_ROUTE_SIGMOID ? ROUTE_SIGMOID : 0) | (groups > 1 && r->group_best == 2 ? ROUTE_BEST2 : 0) |
+            (r->renormalize ? ROUTE_RENORM : 0);
+  a.scale = r->scale;
   return QG_OK;
 }
 
@@ -1094,6 +1179,114 @@ int qg_mx_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const 
   if (mx_quant_blocks(Qdesc->rows * a.cpr, 1) > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (!h->online) return QG_ERR_HIP;
   return launch_mx_dequantize(a, Ydesc->type, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+
+int qg_int_quantize(qg_handle* h, int act, const void* X, const qg_layout* Xdesc, const int32_t* rows, void* Q,
+                   const qg_layout* Qdesc, float* S, const qg_layout* Sdesc, hipStream_t stream) {
+  if (!h || !Xdesc || !Qdesc || !Sdesc) return QG_ERR_INVALID_ARG;
+  if (act != QG_MX_IDENTITY && act != QG_MX_SWIGLU) return QG_ERR_INVALID_ARG;
+  I8QuantArgs a{};
+  // (an empty index array may have no address)
+  const int64_t vrows = rows || Qdesc->rows == 0 ? Xdesc->rows : Qdesc->rows;
+  const int64_t vcols = act == QG_MX_SWIGLU ? 2 * Qdesc->cols : Qdesc->cols;
+  const int st = i8_args(X, Xdesc, vrows, vcols, Q, Qdesc, S, Sdesc, a);
+  if (st != QG_OK) return st;
+  if (!aligned4(rows)) return QG_ERR_ALIGNMENT;
+  if (Qdesc->cols > kI8QuantMaxK) return QG_ERR_UNSUPPORTED;
+  if (Qdesc->rows == 0) return QG_OK;
+  a.rows = rows;
+  if (!h->online) return QG_ERR_HIP;
+  return launch_i8_quantize(a, Xdesc->type, act == QG_MX_SWIGLU, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+int qg_int_dequantize(qg_handle* h, const void* Q, const qg_layout* Qdesc, const float* S, const qg_layout* Sdesc, void* Y,
+                     const qg_layout* Ydesc, hipStream_t stream) {
+  if (!h || !Ydesc || !Qdesc || !Sdesc) return QG_ERR_INVALID_ARG;
+  I8QuantArgs a{};
+  const int st = i8_args(Y, Ydesc, Qdesc->rows, Qdesc->cols, Q, Qdesc, S, Sdesc, a);
+  if (st != QG_OK) return st;
+  if (Qdesc->rows == 0 || Qdesc->cols == 0) return QG_OK;
+  if (!h->online) return QG_ERR_HIP;
+  return launch_i8_dequantize(a, Ydesc->type, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+
+int qg_route(qg_handle* h, const qg_routing* routing, const void* X, const qg_layout* Xdesc, const float* bias, int32_t* ids,
+             const qg_layout* Idesc, float* W, const qg_layout* Wdesc, hipStream_t stream) {
+  if (!h || !routing || !Xdesc || !Idesc || !Wdesc) return QG_ERR_INVALID_ARG;
+  RouteArgs a{};
+  const int st = route_args(routing, X, Xdesc, bias, ids, Idesc, W, Wdesc, a);
+  if (st != QG_OK) return st;
+  if (Xdesc->rows == 0) return QG_OK;
+  if (!h->online) return QG_ERR_HIP;
+  return launch_route(a, Xdesc->type, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+
+int qg_group_rows(qg_handle* h, int experts, const int32_t* ids, const qg_layout* Idesc, int32_t* offsets, int32_t* rows,
+                  int32_t* back, const qg_workspace* ws, hipStream_t stream) {
+  if (!h || !Idesc || experts < 1 || !offsets) return QG_ERR_INVALID_ARG;
+  int st;
+  if ((st = check_layout(Idesc))) return st;
+  if (Idesc->type != QG_I32 || experts > kGroupMaxExperts) return QG_ERR_UNSUPPORTED;
+  if ((st = check_table(ids, Idesc, Idesc->rows, Idesc->cols, true))) return st;
+  const int64_t n = Idesc->rows * Idesc->cols;
+  if (n > kGroupMaxEntries) return QG_ERR_UNSUPPORTED;
+  if (n > 0 && (!rows || !back)) return QG_ERR_INVALID_ARG;
+  if (!aligned4(offsets) || !aligned4(rows) || !aligned4(back)) return QG_ERR_ALIGNMENT;
+  GroupArgs a{};
+  a.ids = ids;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.back = back;
+  a.n = (int32_t)n;
+  a.K = (int32_t)Idesc->cols;
+  a.ldi = (int32_t)Idesc->ld;
+  a.E = experts;
+  group_chunks(n, &a.chunk, &a.chunks);
+  if (a.chunks > 1) {
+    if (!ws || !ws->partials || ws->partials_size < (size_t)a.chunks * experts * 4) return QG_ERR_WORKSPACE;
+    if (!aligned16(ws->partials)) return QG_ERR_ALIGNMENT;
+    a.counts = (int32_t*)ws->partials;
+  }
+  if (!h->online) return QG_ERR_HIP;
+  return launch_group(a, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+}
+
+int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_t* back, const float* W, const qg_layout* Wdesc,
+               float beta, const void* C, const qg_layout* Cdesc, void* Y, const qg_layout* Ydesc, hipStream_t stream) {
+  if (!h || !Rdesc || !Wdesc || !Ydesc) return QG_ERR_INVALID_ARG;
+  int st;
+  if ((st = check_layout(Rdesc)) || (st = check_layout(Wdesc)) || (st = check_layout(Ydesc))) return st;
+  if (!is_float(Rdesc->type) || !is_float(Ydesc->type) || Wdesc->type != QG_F32) return QG_ERR_UNSUPPORTED;
+  if (!std::isfinite(beta)) return QG_ERR_INVALID_ARG;
+  const int64_t T = Ydesc->rows, H = Ydesc->cols, K = Wdesc->cols;
+  if ((st = check_table(Y, Ydesc, T, H)) || (st = check_table(R, Rdesc, Rdesc->rows, H)) || (st = check_table(W, Wdesc, T, K, true)))
+    return st;
+  if (T > 0 && K > 0 && !back) return QG_ERR_INVALID_ARG;
+  if (!aligned4(back)) return QG_ERR_ALIGNMENT;
+  CombineArgs a{};
+  if (beta != 0.f) {
+    if (!Cdesc) return QG_ERR_INVALID_ARG;
+    if ((st = check_layout(Cdesc))) return st;
+    if (!is_float(Cdesc->type)) return QG_ERR_UNSUPPORTED;
+    if ((st = check_table(C, Cdesc, T, H))) return st;
+    a.C = C;
+    a.ldc = (int32_t)Cdesc->ld;
+  }
+  if (T == 0 || H == 0) return QG_OK;
+  a.R = R;
+  a.back = back;
+  a.W = W;
+  a.Y = Y;
+  a.ldr = (int32_t)Rdesc->ld;
+  a.ldw = (int32_t)Wdesc->ld;
+  a.ldy = (int32_t)Ydesc->ld;
+  a.T = (int32_t)T;
+  a.K = (int32_t)K;
+  a.N = (int32_t)Rdesc->rows;
+  a.H = (int32_t)H;
+  a.cpr = (int32_t)cdiv(H, 8);
+  a.beta = beta;
+  if (!h->online) return QG_ERR_HIP;
+  return launch_combine(a, Rdesc->type, beta != 0.f ? Cdesc->type : -1, Ydesc->type, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_plan(qg_handle* h, const qg_operation* op, const qg_layout* Adesc, const qg_layout* Udesc,

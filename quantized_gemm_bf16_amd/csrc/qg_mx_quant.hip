@@ -37,16 +37,13 @@
 
 #include <algorithm>
 
-#include "qg_args.hpp"
-#include "qg_device.hpp"
+#include "qg_rows.hpp"
 
 namespace qg {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-typedef i32x4 __attribute__((aligned(2))) i32x4_u2;
 
 // Rounds two values (already over their scale) to E2M1 codes in byte SEL of a dword.
 template <int SEL>
@@ -68,67 +65,6 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
   return x;
 }
-
-// Eight elements as loaded: one 16-byte chunk of 16-bit values or two of fp32.
-template <int DT>
-struct Raw {
-  static constexpr int ES = DT == DT_F32 ? 4 : 2;
-  i32x4 d[DT == DT_F32 ? 2 : 1];
-  // n of the eight exist (the rest read as zero); p is aligned to 16 bytes
-  // where AL, else to the element
-  template <bool AL>
-  __device__ __forceinline__ void load(const char* p, int n) {
-    if (n >= 8) {
-#pragma unroll
-      for (int i = 0; i < ES / 2; ++i) d[i] = AL ? ((const i32x4*)p)[i] : ((const i32x4_u2*)p)[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < ES / 2; ++i) d[i] = i32x4{};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) {
-          if constexpr (ES == 4)
-            d[j / 4][j % 4] = ((const int*)p)[j];
-          else
-            d[0][j / 2] |= (int)((uint32_t)((const uint16_t*)p)[j] << (16 * (j & 1)));
-        }
-    }
-  }
-  __device__ __forceinline__ float at(int j) const {
-    // (a copy: a bit cast of a vector's element itself would take element 0)
-    const uint32_t w = (uint32_t)(DT == DT_F32 ? d[j / 4][j % 4] : d[0][j / 2]);
-    if constexpr (DT == DT_F32) return __builtin_bit_cast(float, w);
-    if constexpr (DT == DT_BF16) return __builtin_bit_cast(float, j & 1 ? w & 0xFFFF0000u : w << 16);
-    return f16_bits_to_f32((uint16_t)(j & 1 ? w >> 16 : w));
-  }
-};
-
-// Row and unit-in-row of unit `first + off` (off < 2^16): `first` is
-// workgroup-uniform, so its division is done once.
-struct Place {
-  int64_t row;
-  int unit;
-};
-struct Places {
-  int64_t row0;
-  uint32_t u0, cpr, magic;
-  __device__ __forceinline__ Places(int64_t first, int cpr_) : cpr((uint32_t)cpr_) {
-    row0 = first < (int64_t(1) << 32) ? (int64_t)((uint32_t)first / cpr) : first / cpr_;
-    u0 = (uint32_t)(first - row0 * cpr_);
-    // n / cpr = (n * magic) >> 32 is exact for n * cpr < 2^32; a workgroup
-    // crosses at most one row's end where rows have 2^15 units or more
-    magic = cpr > 1 ? 0xFFFFFFFFu / cpr + 1 : 0;
-  }
-  __device__ __forceinline__ Place at(uint32_t off) const {
-    uint32_t n = u0 + off, q;
-    if (cpr >= (1u << 15)) {
-      q = n >= cpr;
-    } else {
-      q = cpr == 1 ? n : __umulhi(n, magic);
-    }
-    return Place{row0 + q, (int)(n - q * cpr)};
-  }
-};
 
 // Codes (low half) and scale byte (high half) of eight values silu(g) u, in 64
 // bits. Called by whole waves: the block's maximum is taken over the quad.
@@ -262,31 +198,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const MxQuantAr
       v[2 * h + 1] = y[1] * scale;
     }
     const int k = at[i].unit * 8;
-    const int64_t base = at[i].row * a.ldx + k;
-    if constexpr (DT == DT_F32) {
-      float* y = (float*)a.X + base;
-      if (k + 8 <= a.K) {
-        // two accesses that each fill half of every line: merged in the L2
-        ((f32x4*)y)[0] = f32x4{v[0], v[1], v[2], v[3]};
-        ((f32x4*)y)[1] = f32x4{v[4], v[5], v[6], v[7]};
-      } else {
-        for (int j = 0; j < 8; ++j)
-          if (k + j < a.K) y[j] = v[j];
-      }
-    } else {
-      uint16_t* y = (uint16_t*)a.X + base;
-      uint32_t h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = DT == DT_BF16 ? f32_to_bf16_bits(v[j]) : f32_to_f16_bits(v[j]);
-      if (k + 8 <= a.K) {
-        const i32x4 p = {(int)(h[0] | h[1] << 16), (int)(h[2] | h[3] << 16), (int)(h[4] | h[5] << 16),
-                         (int)(h[6] | h[7] << 16)};
-        __builtin_nontemporal_store(p, (i32x4*)y);
-      } else {
-        for (int j = 0; j < 8; ++j)
-          if (k + j < a.K) y[j] = (uint16_t)h[j];
-      }
-    }
+    store8<DT, true>((char*)a.X + (at[i].row * a.ldx + k) * Raw<DT>::ES, v, a.K - k);
   }
 }
 

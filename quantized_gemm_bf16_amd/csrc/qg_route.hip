@@ -1,0 +1,332 @@
+// Choice of experts: one wave per token.
+//
+// Score p = softmax(x) or sigmoid(x); key = p + bias, or x itself where there is
+// no bias (the same order, and exact). A group's standing is its best key or
+// the sum of its two best; the best groups keep their experts; the K best
+// keys are chosen, ties to the lowest index.
+//
+// Lane l holds NV consecutive experts of group l >> shift, so that lane order is
+// index order, a group is an aligned run of lanes, and the lowest lane of a
+// ballot is the lowest index. A round of the choice is a wave-wide maximum of
+// the keys as ordered integers, a ballot for its place, and the removal of that key.
+//
+// Keys are those of 64-bit arithmetic: fp32 decides where two neighbours in the
+// order (or the groups on both sides of the cut) are further apart than the
+// errors of their keys, or have the same key (equal logit, equal bias); a
+// token where they are not is done again in 64 bits, by its wave. Errors of an
+// fp32 score, relative, in 2^-23, exp2 and rcp being good to 1 each: e^x is off
+// by 0.61 |x| (the product's rounding, the constant's) + 1. Sigmoid: (1 - s) of that (what
+// e does to 1 / (1 + e)), 0.5 for the sum, 1 for rcp: at most 4 + |x| (1 - s). Softmax: its
+// own e^x and the sum's (weighted, so less than the largest |x| e^x, under 0.4), 11 for the
+// sum's 22 roundings (16 serially, then a tree), 2 for rcp and the product: at most 16 + 1.5 |x|.
+#include "qg_experts.hpp"
+
+#include <algorithm>
+
+#include "qg_args.hpp"
+#include "qg_device.hpp"
+
+namespace qg {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504f;
+constexpr float kMinusInf = -__builtin_inff();
+
+// x of the lanes that DPP control CTRL shifts in, `none` where there is none
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t none, uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, CTRL, 0xF, 0xF, false);
+}
+// Row shifts by 1, 2, 4, 8, then the broadcasts of lane 15 and lane 31: lane 63 has seen every lane.
+template <class F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t none, uint32_t x, F f) {
+  x = f(x, dpp<0x111>(none, x));
+  x = f(x, dpp<0x112>(none, x));
+  x = f(x, dpp<0x114>(none, x));
+  x = f(x, dpp<0x118>(none, x));
+  x = f(x, dpp<0x142>(none, x));
+  x = f(x, dpp<0x143>(none, x));
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  return wave_reduce(0, x, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t x) {
+  for (int d = 1; d < 64; d <<= 1) x = max(x, (uint64_t)__shfl_xor((unsigned long long)x, d, 64));
+  return x;
+}
+// (row_bcast sums rows 0 and 1 into row 1, and so on: every lane's value is in lane 63's sum once)
+__device__ __forceinline__ float wave_sum(float x) {
+  return __builtin_bit_cast(float, wave_reduce(0, __builtin_bit_cast(uint32_t, x), [](uint32_t a, uint32_t b) {
+                              return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+                            }));
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d, 64);
+  return x;
+}
+
+// Integers in the order of the floating values (0 is below all of them; -0 and +0 are one).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __builtin_bit_cast(float, k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+__device__ __forceinline__ uint64_t ordered(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+
+template <int DT>
+__device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
+  if constexpr (DT == DT_F32) return ((const float*)a.X)[t * a.ldx + e];
+  const uint16_t h = ((const uint16_t*)a.X)[t * a.ldx + e];
+  return DT == DT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+}
+
+// The `rounds` best keys (0: not there): lane r gets the expert of the r-th, -1 where fewer are there.
+template <class Key, int NV>
+__device__ __forceinline__ int choose(Key (&key)[NV], int e0, int rounds, int& found) {
+  const int lane = lane_id();
+  int mine = -1;
+  found = 0;
+  for (int r = 0; r < rounds; ++r) {
+    Key top = key[0];
+#pragma unroll
+    for (int j = 1; j < NV; ++j) top = max(top, key[j]);
+    top = wave_max(top);
+    if (top == 0) break;
+    uint64_t at[NV], any = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) any |= at[j] = __ballot(key[j] == top);
+    const int w = __builtin_ctzll(any);
+    int first = NV - 1;
+#pragma unroll
+    for (int j = NV - 2; j >= 0; --j)
+      if (at[j] >> w & 1) first = j;
+    const int e = __builtin_amdgcn_readlane(e0, w) + first;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (lane == w && j == first) key[j] = 0;
+    if (lane == r) mine = e;
+    ++found;
+  }
+  return mine;
+}
+
+// A lane's group standing from its own keys' two best, over the run of lanes that holds the group.
+template <class F>
+__device__ __forceinline__ F standing(F b1, F b2, int shift, bool best2) {
+  for (int d = 1; d < 1 << shift; d <<= 1) {
+    const F o1 = __shfl_xor(b1, d, 64), o2 = __shfl_xor(b2, d, 64);
+    const F low = b1 < o1 ? b1 : o1;
+    b1 = b1 < o1 ? o1 : b1;
+    b2 = b2 < o2 ? o2 : b2;
+    b2 = b2 < low ? low : b2;
+  }
+  return best2 && b2 > (F)kMinusInf ? b1 + b2 : b1;
+}
+
+// The choice in 64 bits.
+template <int DT, int NV>
+__device__ __attribute__((noinline)) int choose64(const RouteArgs& a, int64_t t, int e0, int count, int& found) {
+  double p[NV], x[NV];
+  double m = kMinusInf;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    x[j] = kMinusInf;
+    if (j < count) x[j] = logit<DT>(a, t, e0 + j);
+    if (!(x[j] > kMinusInf)) x[j] = kMinusInf;
+    m = x[j] > m ? x[j] : m;
+  }
+  if (a.flags & ROUTE_SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) p[j] = 1.0 / (1.0 + exp(-x[j]));
+  } else {
+    for (int d = 1; d < 64; d <<= 1) {
+      const double o = __shfl_xor(m, d, 64);
+      m = o > m ? o : m;
+    }
+    double sum = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) sum += p[j] = !(x[j] > kMinusInf) ? 0.0 : x[j] == m ? 1.0 : exp(x[j] - m);
+    sum = wave_sum(sum);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) p[j] /= sum;
+  }
+  uint64_t key[NV];
+  double b1 = kMinusInf, b2 = kMinusInf;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    double s = p[j], k = x[j];
+    if (a.bias && j < count) k = s += a.bias[e0 + j];
+    const bool there = x[j] > kMinusInf && k > kMinusInf;
+    key[j] = there ? ordered(k) : 0;
+    if (!(a.flags & ROUTE_BEST2)) s = k;
+    if (!there) s = kMinusInf;
+    b2 = s > b1 ? b1 : s > b2 ? s : b2;
+    b1 = s > b1 ? s : b1;
+  }
+  if (a.groups > 1) {
+    const double st = standing(b1, b2, a.shift, (a.flags & ROUTE_BEST2) != 0);
+    const int mine = lane_id() >> a.shift;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double o = __shfl(st, g << a.shift, 64);
+      before += o > st || (o == st && g < mine);
+    }
+    if (before >= a.kept) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] = 0;
+    }
+  }
+  return choose(key, e0, a.K, found);
+}
+
+template <int DT, int NV>
+__global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
+  const int lane = lane_id();
+  const int run = 1 << a.shift, g = lane >> a.shift, e0 = g * a.per + (lane & (run - 1)) * NV;
+  const int count = g < a.groups ? max(0, min(NV, a.per - (lane & (run - 1)) * NV)) : 0;
+  const bool sigmoid = a.flags & ROUTE_SIGMOID, best2 = a.flags & ROUTE_BEST2, renorm = a.flags & ROUTE_RENORM;
+  const bool scores = a.bias || best2;  // the choice looks at the scores, not the logits alone
+  for (int64_t t = (int64_t)blockIdx.x * 4 + wave_id(); t < a.T; t += (int64_t)gridDim.x * 4) {
+    float x[NV];
+    float m = kMinusInf, total = 1.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      x[j] = kMinusInf;
+      if (j < count) x[j] = logit<DT>(a, t, e0 + j);
+      if (!(x[j] > kMinusInf)) x[j] = kMinusInf;  // NaN too
+      m = fmaxf(m, x[j]);
+    }
+    const auto score = [&](float v) {  // without the softmax's 1 / total
+      if (sigmoid) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -kLog2e));
+      return v == m ? 1.f : __builtin_amdgcn_exp2f((v - m) * kLog2e);
+    };
+    float p[NV];
+    if (!sigmoid && (scores || !renorm)) {
+      const uint32_t k = wave_max(m > kMinusInf ? ordered(m) : 0);
+      m = k ? unordered(k) : kMinusInf;
+      float sum = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) sum += p[j] = x[j] > kMinusInf ? score(x[j]) : 0.f;
+      total = __builtin_amdgcn_rcpf(wave_sum(sum));
+    }
+    uint32_t key[NV];
+    float b1 = kMinusInf, b2 = kMinusInf;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float s = 0.f, k = x[j];
+      if (scores) s = sigmoid ? score(x[j]) : p[j] * total;
+      if (a.bias && j < count) k = s += a.bias[e0 + j];
+      const bool there = x[j] > kMinusInf && k > kMinusInf;
+      key[j] = there ? ordered(k) : 0;
+      if (!best2) s = k;
+      if (!there) s = kMinusInf;
+      b2 = s > b1 ? b1 : fmaxf(s, b2);
+      b1 = fmaxf(s, b1);
+    }
+    bool unsure = false;
+    if (a.groups > 1) {
+      const float st = standing(b1, b2, a.shift, best2);
+      // How far the standings of this group and another may be off together. With a bias: two scores each
+      // (at most 5, or 16, times 2^-23), and the roundings of four keys and two sums. Without: scores of
+      // up to e^-88 (smaller ones are zero), relative.
+      float tol = st * 0x1p-14f + 0x1p-120f;
+      if (a.bias) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) most = max(most, key[j] ? __builtin_bit_cast(uint32_t, unordered(key[j])) & 0x7FFFFFFFu : 0);
+        tol = (sigmoid ? 0x1p-18f : 0x1p-17f) + __builtin_bit_cast(float, wave_max(most)) * 0x1p-21f;
+      }
+      int sure = 0, maybe = 0;
+      for (int o = 0; o < a.groups; ++o) {
+        const float other = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, st), o << a.shift));
+        const bool first = o < g;
+        if (scores && st > kMinusInf) {
+          sure += other > st + tol;
+          maybe += o != g && !(other < st - tol);
+        } else {
+          const bool before = other > st || (other == st && first);
+          sure += before;
+          maybe += before;
+        }
+      }
+      unsure = g < a.groups && maybe >= a.kept && sure < a.kept;
+      if (maybe >= a.kept) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) key[j] = 0;
+      }
+    }
+    int found = 0, mine = -1;
+    float l = 0.f;
+    bool redo = __any(unsure);
+    if (!redo) {
+      mine = choose(key, e0, a.bias ? a.K + 1 : a.K, found);
+      if (mine >= 0) l = logit<DT>(a, t, mine);
+      if (a.bias) {
+        // every key against the next one: too near to call, and not the same expert twice?
+        const float b = mine >= 0 ? a.bias[mine] : 0.f, s = score(l) * total, k = s + b;
+        const float rel = sigmoid ? 4.f + fminf(fabsf(l), 128.f) * (1.f - s) : 16.f + (l == m ? 0.f : 1.5f * fminf(m - l, 128.f));
+        const float err = (s * rel + fabsf(k)) * 0x1p-23f + 0x1p-120f;
+        const float ln = __shfl_down(l, 1, 64), bn = __shfl_down(b, 1, 64), kn = __shfl_down(k, 1, 64), en = __shfl_down(err, 1, 64);
+        redo = __any(lane + 1 < found && !(k - kn > err + en) && !(l == ln && b == bn));
+      }
+    }
+    if (redo) {
+      mine = choose64<DT, NV>(a, t, e0, count, found);
+      if (mine >= 0) l = logit<DT>(a, t, mine);
+    }
+    const bool have = mine >= 0 && lane < a.K;
+    float w = have ? score(l) * total : 0.f;
+    if (renorm) {
+      float sum = wave_sum(sigmoid ? w : 0.f);
+      if (!sigmoid || sum < 0x1p-80f) {
+        // relative to the best of the chosen: softmax by its definition, sigmoids as small as that within 2^-80 of it
+        const uint32_t k = wave_max(have ? ordered(l) : 0);
+        const float best = k ? unordered(k) : 0.f;
+        w = !have ? 0.f : l == best ? 1.f : __builtin_amdgcn_exp2f((l - best) * kLog2e);
+        sum = wave_sum(w);
+      }
+      w = sum > 0.f ? w / sum : 0.f;
+    }
+    if (lane < a.K) {
+      a.ids[t * a.ldi + lane] = have ? mine : -1;
+      a.W[t * a.ldw + lane] = have ? w * a.scale : 0.f;
+    }
+  }
+}
+
+template <int DT, int NV>
+hipError_t route_nv(const RouteArgs& a, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>((a.T + 3) / 4, 1 << 20);
+  hipLaunchKernelGGL((route_kernel<DT, NV>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t route_t(const RouteArgs& a, hipStream_t s) {
+  const int nv = (a.per + (1 << a.shift) - 1) >> a.shift;
+  if (nv <= 1) return route_nv<DT, 1>(a, s);
+  if (nv <= 2) return route_nv<DT, 2>(a, s);
+  if (nv <= 4) return route_nv<DT, 4>(a, s);
+  if (nv <= 8) return route_nv<DT, 8>(a, s);
+  return route_nv<DT, 16>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, int x_type, hipStream_t s) {
+  switch (x_type) {
+    case DT_F32: return route_t<DT_F32>(a, s);
+    case DT_F16: return route_t<DT_F16>(a, s);
+    case DT_BF16: return route_t<DT_BF16>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace qg

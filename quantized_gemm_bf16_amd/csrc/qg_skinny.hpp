@@ -389,7 +389,7 @@ struct Skinny {
         const int n = u.n0 + nw0 + tn * 16 + 4 * (l >> 4);
         if (n >= a.N) continue;
         if constexpr (Cfg::INT)
-          epi_store4(a, m, n, acc.v[tn][mt]);
+          epi_store4(a, u.expert, m, n, acc.v[tn][mt]);
         else
           epi_store4c(a, m, n, acc.v[tn][mt], acc.c[tn][mt]);
       }

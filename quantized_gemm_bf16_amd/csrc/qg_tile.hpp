@@ -209,11 +209,11 @@ __device__ __forceinline__ void epi_store4(const Args& a, int64_t m, int n, cons
 
 // int8 path: D = acc (+ C when beta == 1), exact int32; with per-row scales
 // of A and B (w8a8) the exact sum is scaled in fp32 and takes the float
-// epilogue: x = acc * U[m] * V[n].
-__device__ __forceinline__ void epi_store4(const Args& a, int64_t m, int n, const i32x4& acc) {
+// epilogue: x = acc * U[m] * V[n], V being the expert's.
+__device__ __forceinline__ void epi_store4(const Args& a, int expert, int64_t m, int n, const i32x4& acc) {
   if (a.int_scaled) {
     const float sa = ((const float*)a.U)[m * a.ldu];
-    const float* vb = (const float*)a.V;
+    const float* vb = (const float*)a.V + expert * a.v_batch;
     f32x4 x;
     for (int j = 0; j < 4; ++j) x[j] = (n + j < a.N) ? (float)acc[j] * sa * vb[(int64_t)(n + j) * a.ldv] : 0.f;
     float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -550,7 +550,10 @@ struct Tile {
           const int n = u.n0 + wn * Cfg::WTN + tn * 32 + 8 * g + 4 * (l >> 5);
           if (n >= a.N) continue;
           S4 v = {acc.v[tn][tm][4 * g], acc.v[tn][tm][4 * g + 1], acc.v[tn][tm][4 * g + 2], acc.v[tn][tm][4 * g + 3]};
-          epi_store4(a, m, n, v);
+          if constexpr (Cfg::INT)
+            epi_store4(a, u.expert, m, n, v);
+          else
+            epi_store4(a, m, n, v);
         }
     }
   }
