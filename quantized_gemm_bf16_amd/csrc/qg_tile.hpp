@@ -470,10 +470,42 @@ struct Tile {
   static constexpr int WROWB = Cfg::WTN * 2;  // bytes of one staged row
   static constexpr int WCH = WROWB / 16;      // 16-byte chunks per staged row
   static constexpr int WRPI = 64 / WCH;       // staged rows per 64-lane read
-  static constexpr bool STAGED = !Cfg::INT && WCH >= 4 && WCH <= 16 &&
+  static constexpr bool STAGED = WCH >= 4 && WCH <= 16 &&
                                  Cfg::NW * Cfg::WTM * WROWB <= Cfg::STAGES * Cfg::STAGE_BYTES;
   __device__ __forceinline__ static bool plain16(const Args& a) {
     return (a.d_type == DT_BF16 || a.d_type == DT_F16) && (a.c_type < 0 || a.beta == 0.f) && a.epi == 0;
+  }
+
+  // w8a8: the exact sums become the fp32 values acc * U[m] * V[n], their bits in place. A column's scale is loaded
+  // once for all of the wave's rows (in the store loop of every output, as the skinny kernels have it, the loads kept the
+  // 256 x 256 tile of 4096^3 for 50 us, as long as its mainloop).
+  __device__ __forceinline__ static void scale_sums(const Args& a, const Unit& u, Acc& acc) {
+    const int w = wave_id(), l = lane_id();
+    const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
+    const float* vb = (const float*)a.V + u.expert * a.v_batch;
+    float sa[TM];
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      const int m = u.m0 + wm * Cfg::WTM + tm * 32 + (l & 31);
+      sa[tm] = m < u.m_end ? ((const float*)a.U)[(int64_t)m * a.ldu] : 0.f;
+    }
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int n = u.n0 + wn * Cfg::WTN + tn * 32 + 8 * (i / 4) + 4 * (l >> 5) + i % 4;
+        const float sb = n < a.N ? vb[(int64_t)n * a.ldv] : 0.f;
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+          const int sum = acc.v[tn][tm][i];
+          acc.v[tn][tm][i] = __builtin_bit_cast(int, (float)sum * sa[tm] * sb);
+        }
+      }
+  }
+  // An accumulator element as fp32 (int8 tiles: after scale_sums)
+  __device__ __forceinline__ static float value(const Acc& acc, int tn, int tm, int i) {
+    const auto x = acc.v[tn][tm][i];
+    return __builtin_bit_cast(float, x);
   }
 
   // DRAIN: the call ends only when the stores have completed; without, they
@@ -494,7 +526,7 @@ struct Tile {
           uint16_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float x = a.alpha * acc.v[tn][tm][4 * g + j];
+            const float x = a.alpha * value(acc, tn, tm, 4 * g + j);
             h[j] = bf ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
           }
           const int ch = tn * 4 + g;
@@ -531,12 +563,32 @@ struct Tile {
 
   // Final results of a tile: epilogue + masked store.
   __device__ __forceinline__ static void store(const Args& a, const Unit& u, Acc& acc, char* smem) {
+    const bool scaled = Cfg::INT && a.int_scaled;
+    if (scaled) scale_sums(a, u, acc);
     if constexpr (STAGED) {
-      if (plain16(a)) {
+      if (plain16(a) && (!Cfg::INT || scaled)) {
         store_staged(a, u, acc, smem);
         return;
       }
     }
+    // (one loop per kind of sum, so that the choice is not made for every four outputs)
+    if constexpr (Cfg::INT) {
+      if (!scaled) {
+        each4(a, u, [&](int m, int n, int tn, int tm, int g) {
+          epi_store4(a, 0, m, n, S4{acc.v[tn][tm][4 * g], acc.v[tn][tm][4 * g + 1], acc.v[tn][tm][4 * g + 2], acc.v[tn][tm][4 * g + 3]});
+        });
+        return;
+      }
+    }
+    each4(a, u, [&](int m, int n, int tn, int tm, int g) {
+      epi_store4(a, m, n,
+                 f32x4{value(acc, tn, tm, 4 * g), value(acc, tn, tm, 4 * g + 1), value(acc, tn, tm, 4 * g + 2), value(acc, tn, tm, 4 * g + 3)});
+    });
+  }
+
+  // f(m, n, tn, tm, g) for the lane's groups of four columns inside the matrix
+  template <class F>
+  __device__ __forceinline__ static void each4(const Args& a, const Unit& u, F f) {
     const int w = wave_id(), l = lane_id();
     const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
 #pragma unroll
@@ -548,12 +600,7 @@ struct Tile {
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int n = u.n0 + wn * Cfg::WTN + tn * 32 + 8 * g + 4 * (l >> 5);
-          if (n >= a.N) continue;
-          S4 v = {acc.v[tn][tm][4 * g], acc.v[tn][tm][4 * g + 1], acc.v[tn][tm][4 * g + 2], acc.v[tn][tm][4 * g + 3]};
-          if constexpr (Cfg::INT)
-            epi_store4(a, u.expert, m, n, v);
-          else
-            epi_store4(a, m, n, v);
+          if (n < a.N) f(m, n, tn, tm, g);
         }
     }
   }
