@@ -47,6 +47,7 @@ struct Args {
   int32_t sk_work;           // stream-K: k-iterations of the remaining tiles, shared evenly
   int32_t group_m;           // tile-order super-group height (in tiles)
   int32_t grid;              // workgroups launched
+  int32_t ahead;             // the operands pass the memory-side cache (big int8 tiles)
   int32_t* counters;         // barriers workspace: one int32 per output tile
   void* partials;            // partials workspace
 

@@ -36,6 +36,7 @@ namespace {
 const char* kVersion = "qgemm 0.1.0";
 const size_t kBarriersSize = size_t(1) << 20;
 const size_t kPartialsSize = size_t(32) << 20;
+const double kMemorySideCache = 256.0 * (1 << 20);
 const int kTuningSeq[] = {1,   2,   4,   8,    16,   24,   32,   48,   64,   96,   128,  192,
                           256, 384, 512, 768, 1024, 1536, 2048, 3072, 4096, 6144, 8192};
 
@@ -599,10 +600,12 @@ int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_wo
     a.tiles_m = (int32_t)(cdiv(p.M, k.bm) + p.E);  // upper bound on the padded m-tiles
     const int64_t ub = (int64_t)a.tiles_m * a.tiles_n;
     pl.tiles = (int)std::min<int64_t>(ub, INT32_MAX);
-    // two workgroups per CU; three of the MXFP4 skinny kernel with a shared A,
-    // whose LDS lets them be resident (128 experts, 95 rows, N 5120, K 468: 37 us, 50
-    // with two of a deeper ring)
-    const int per_cu = k.family == FAM_MX_SKINNY && k.bn == 64 ? 3 : 2;
+    // two workgroups per CU; three of the MXFP4 and int8 skinny kernels with a shared A,
+    // whose LDS lets them be resident (128 experts, 95 rows, N 5120, K 468, MXFP4: 37 us, 50
+    // with two of a deeper ring; int8: 47, 59 with two, 58 with four); one of the other int8 kernels, as
+    // their LDS allows (64 experts, 65536 rows, N 2048, K 7168: 1130 us, 1190 with two)
+    const bool shared_a = k.bn == 64 && (k.family == FAM_MX_SKINNY || (k.family == FAM_SKINNY && p.ta == QG_I8));
+    const int per_cu = shared_a ? 3 : p.ta == QG_I8 ? 1 : 2;
     pl.grid = (int)std::max<int64_t>(1, std::min<int64_t>(ub, (int64_t)h->cus * per_cu));
     pl.c.split = 1;
     pl.c.programs = 0;
@@ -658,6 +661,10 @@ int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_wo
     a.counters = (int32_t*)ws->barriers;
   }
   a.grid = pl.grid;
+  if (p.ta == QG_I8) {
+    const double a_bytes = (double)p.M * p.lda * (p.batched ? p.E : 1), b_bytes = (double)p.N * p.ldb * (p.E > 0 && p.b_batch ? p.E : 1);
+    a.ahead = a_bytes + b_bytes > kMemorySideCache;
+  }
   return QG_OK;
 }
 
@@ -675,6 +682,7 @@ int skinny_for(const Problem& p, int64_t target_bn) {
   for (int i = 0; i < kNumKernels; ++i) {
     const KernelInfo& k = kKernels[i];
     if (k.family != FAM_SKINNY || !compatible(k, p)) continue;
+    if (k.in_type == DT_I8 && k.bn == 64) continue;  // small workgroups for experts (i8_grouped)
     if (best < 0) {
       best = i;
       continue;
@@ -753,6 +761,33 @@ Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws
   return c;
 }
 
+// int8 over experts. Up to 16 rows on average stream B through small workgroups that share A (three per CU), more take the
+// tile with the least estimated time: a CU that has n tiles takes n (fixed + step per 128 of K). Measured, us, skinny
+// 16 x 64 / tiles of 32 x 128 / 128 x 128 / 256 x 256:
+//   64 experts, N 2048, K 7168:    128 rows 153 / 162 / 200 / 219    1024 rows  179 / 189 / 189 / 241
+//                                 4096 rows 346 / 297 / 240 / 255    8192 rows  557 / 495 / 289 / 342
+//                                16384 rows   - / 939 / 456 / 368
+//   256 experts, 4096 rows, N 1536, K 2048    169 / 176 / 208 / 225   8 experts, 200 rows, N, K 4096   30 / 27 / 30 / 47
+//   24 experts, 1501 rows, N 1000, K 2075      30 / 29 / 24 / 38      128 experts, 95 rows, N 5120, K 468   48 / 97 / 142 / 112
+//   8 experts, 1000 rows, N 14336, K 4096     315 / 275 / 156 / 161   32 experts, 40000 rows, N 1408, K 2048   - / 554 / 271 / 160
+int i8_grouped(const qg_handle* h, const Problem& p) {
+  if (p.M <= (int64_t)16 * p.E) return kernel_by_shape(p, 16, 64);
+  static const struct {
+    int bm, bn;
+    double fixed, step;
+  } kTiles[] = {{32, 128, 2.5, 0.35}, {128, 128, 4, 0.62}, {256, 256, 9, 1.9}};
+  const double live = (double)std::min<int64_t>(p.E, p.M);
+  int kernel = -1;
+  double best = 0;
+  for (const auto& t : kTiles) {
+    // m-tiles: every expert that has rows ends inside a tile half the time
+    const double tm = std::max(live, (double)cdiv(p.M, t.bm) + live / 2);
+    const double us = std::max(1.0, std::ceil(tm * (double)cdiv(p.N, t.bn) / h->cus)) * (t.fixed + (double)cdiv(p.K, 128) * t.step);
+    if (kernel < 0 || us < best) kernel = kernel_by_shape(p, t.bm, t.bn), best = us;
+  }
+  return kernel;
+}
+
 // Shape heuristic used on a cache miss. `mode` / `split` are the schedule the
 // caller forces (MODE_DP with split 0 = nothing forced).
 Choice heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, int forced_mode = -1,
@@ -773,6 +808,11 @@ Choice heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws, i
     if (c.kernel < 0)
       c.kernel = kernel_by_shape(p, p.M >= 256 && p.N >= 256 ? 256 : 128, p.M >= 256 && p.N >= 256 ? 256 : 128);
     if (c.kernel < 0) c.kernel = kernel_by_shape(p, 128, 128);
+    return c;
+  }
+  if (p.E > 0 && p.ta == QG_I8) {
+    c.kernel = i8_grouped(h, p);
+    c.mode = MODE_GROUPED;
     return c;
   }
   if (p.E > 0) {

@@ -63,9 +63,6 @@ __device__ __forceinline__ f32x4 mfma16_bf16(i32x4 a, i32x4 b, f32x4 c) {
 __device__ __forceinline__ f32x4 mfma16_f16(i32x4 a, i32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ i32x4 mfma16_i8(i32x4 a, i32x4 b, i32x4 c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
-}
 
 template <class Cfg>
 struct Skinny {

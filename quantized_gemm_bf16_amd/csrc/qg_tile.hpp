@@ -33,13 +33,19 @@ struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WAVES_M = WM_, WAVES_N = WN_, STAGES = STAGES_;
   static constexpr int NW = WM_ * WN_, NT = NW * 64;
   static constexpr int WTM = BM / WM_, WTN = BN / WN_;
-  static constexpr int TM = WTM / 32, TN = WTN / 32;
+  // MFMA block: the big int8 tiles, bound by power, take 16 x 16 x 64, which draws less per operation than 32 x 32 x 32
+  // (a loop of nothing else on random operands, 8 waves per CU: 4.2 against 3.3 POPS; both reach 4.9 on zeros). The
+  // small ones, one wave per SIMD, have more time between a fragment's read and its use with 32 x 32 (128 x 128: 1435
+  // shader cycles per k-tile, 1750 with 16 x 16).
+  static constexpr int MB = (E_ == El::I8 && WTM >= 128) ? 16 : 32;
+  static constexpr int TM = WTM / MB, TN = WTN / MB;
+  static constexpr int G = MB == 32 ? 4 : 1;             // groups of 4 consecutive columns that a lane holds of a block
   static constexpr int ESIZE = (E_ == El::BF16 || E_ == El::F16) ? 2 : 1;
   static constexpr int CH = (E_ == El::E4M3) ? 2 : 1;  // 16-byte chunks per lane per MFMA
   static constexpr int ROWB = ROWB_;
   static constexpr int CPR = ROWB / 16;                  // 16-byte chunks per row
   static constexpr int RPI = 64 / CPR;                   // rows filled by one 64-lane load
-  static constexpr int KSTEPS = CPR / (2 * CH);          // MFMAs along k per k-tile
+  static constexpr int KSTEPS = CPR / (MB == 32 ? 2 * CH : 4);  // MFMAs along k per k-tile
   static constexpr int BK = ROWB / ESIZE;                // elements per k-tile
   static constexpr int A_BYTES = BM * ROWB, B_BYTES = BN * ROWB;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -54,20 +60,30 @@ struct TileCfg {
   static_assert(2 * LPW * (STAGES - 1) < 64, "vmcnt range (the first half of the waves issues all loads)");
 };
 
-template <bool INT>
+template <bool INT, int MB = 32>
 struct AccOf;
 template <>
-struct AccOf<false> {
+struct AccOf<false, 32> {
   using V = f32x16;
   using S = float;
   using S4 = f32x4;
 };
 template <>
-struct AccOf<true> {
+struct AccOf<true, 32> {
   using V = i32x16;
   using S = int;
   using S4 = i32x4;
 };
+template <>
+struct AccOf<true, 16> {
+  using V = i32x4;
+  using S = int;
+  using S4 = i32x4;
+};
+
+__device__ __forceinline__ i32x4 mfma16_i8(i32x4 a, i32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
 
 // XOR key of a row's 16-byte chunks in LDS: 16 consecutive rows must cover
 // the 16 bank groups of 256 bytes; a row holds CPR chunks, so rows r and
@@ -254,16 +270,28 @@ __device__ __forceinline__ void interleave_reads() {
 // ---- the kernel body -----------------------------------------------------
 template <class Cfg>
 struct Tile {
-  using AO = AccOf<Cfg::INT>;
+  using AO = AccOf<Cfg::INT, Cfg::MB>;
   using AccV = typename AO::V;
   using S4 = typename AO::S4;
   static constexpr int TN = Cfg::TN, TM = Cfg::TM;
-  static constexpr int NQ = TN * TM * 4;  // 4-element groups per lane
+  static constexpr int MB = Cfg::MB, G = Cfg::G;
+  static constexpr int NQ = TN * TM * G;  // 4-element groups per lane
   static constexpr int BM = Cfg::BM, BN = Cfg::BN, NT = Cfg::NT;
-  static constexpr int SMEM_BYTES = Cfg::STAGES * Cfg::STAGE_BYTES;
+  // Operands that the memory-side cache does not hold (Args::ahead): one wave of a big int8 tile touches lines of the
+  // k-tiles behind the ring, a part of them, the other parts being its neighbours' that read the same rows, so that
+  // they are in the L2 when the ring asks for them. Its two stages cover the L2's latency, not that of HBM (shader cycles
+  // per k-tile: 2650 from the memory-side cache, 3600 from HBM without this, 3070 with; it costs the former 300).
+  // 64 experts, 65536 rows, N 2048, K 7168: 968 us, 1040 without, 995 one k-tile ahead of the ring, 1004 four.
+  static constexpr int AHEAD = Cfg::INT && BM == 256 ? 2 : 0;
+  static constexpr int SMEM_BYTES = Cfg::STAGES * Cfg::STAGE_BYTES + (AHEAD ? 256 : 0);
   struct Acc {
     AccV v[TN][TM];
   };
+  static constexpr bool GROUPED_XCD = Cfg::INT && BM == 256;
+
+  // Row and first column, in the wave's tile, of group g of block (tn, tm) of a lane.
+  __device__ __forceinline__ static int row_of(int tm, int l) { return tm * MB + (l & (MB - 1)); }
+  __device__ __forceinline__ static int col_of(int tn, int g, int l) { return tn * MB + 8 * g + 4 * (l / MB); }
 
   __device__ __forceinline__ static void mainloop(const Args& a, const Unit& u, char* smem, Acc& acc) {
     const int w = wave_id(), l = lane_id();
@@ -312,7 +340,19 @@ struct Tile {
                   "the second half's rows keep the swizzle key (period 16 rows)");
     const uint32_t stepA = (uint32_t)(HALF * Cfg::LA * RPI * lda_b), stepB = (uint32_t)(HALF * Cfg::LB * RPI * ldb_b);
     auto issue = [&](int stage, int kt) {
-      if (w >= HALF) return;
+      if (w >= HALF) {
+        if constexpr (AHEAD > 0) {
+          // a dword per line, to LDS that nobody reads (the first half of the waves alone waits for its loads)
+          if (a.ahead && w == HALF && kt + AHEAD < u.ke) {
+            char* nowhere = smem + Cfg::STAGES * Cfg::STAGE_BYTES;
+            const uint32_t kk = (uint32_t)(kt + AHEAD) * ROWB;
+            const int ra = (u.n0 / BN % 8) * (BM / 8) + l, rb = (u.m0 / BM % 4) * (BN / 4) + l;
+            load_lds_x1a(rA, nowhere, l < BM / 8 ? (uint32_t)(ra * lda_b) + kk : kOOB);
+            load_lds_x1a(rB, nowhere, l < BN / 4 ? (uint32_t)(rb * ldb_b) + kk : kOOB);
+          }
+        }
+        return;
+      }
       char* sbase = smem + stage * Cfg::STAGE_BYTES;
       const uint32_t kk = (uint32_t)kt * ROWB;
       const bool live = kt < u.ke;
@@ -365,6 +405,76 @@ struct Tile {
       }
     };
 
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) acc.v[tn][tm] = AccV{};
+
+    const int nk = u.ke - u.kb;
+    constexpr int S = Cfg::STAGES, KS = Cfg::KSTEPS;
+    // Prologue: fill all S stages, wait for the first.
+#pragma unroll
+    for (int st = 0; st < S; ++st) issue(st, u.kb + st);
+    wait_vmcnt<2 * Cfg::LPW * (S - 1)>();  // the loading waves hold 2 LPW loads per stage
+    if (u.kb == ktail) trim(0, ktail);
+    lds_barrier();
+    if constexpr (MB == 16) {
+      // A k-step's fragments (TM of A, TN of B) do not fit twice beside the accumulators: A comes in halves, each half
+      // and the next k-step's B being read while the half before is multiplied.
+      constexpr int H = TM / 2;
+      auto frag = [&](const char* base, int row, int ks) {
+        return *(const i32x4*)(base + row * ROWB + (((ks * 4 + (l >> 4)) ^ swz<CPR>(row)) << 4));
+      };
+      auto read_a = [&](int stage, int ks, int h, i32x4 (&f)[H]) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) f[i] = frag(smem + stage * Cfg::STAGE_BYTES, wm * Cfg::WTM + row_of(h * H + i, l), ks);
+      };
+      auto read_b = [&](int stage, int ks, i32x4 (&f)[TN]) {
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) f[tn] = frag(smem + stage * Cfg::STAGE_BYTES + Cfg::A_BYTES, wn * Cfg::WTN + row_of(tn, l), ks);
+      };
+      auto mma = [&](const i32x4 (&fa)[H], const i32x4 (&fb)[TN], int h, int tn0, int tn1) {
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+          for (int i = 0; i < H; ++i)
+            if (tn >= tn0 && tn < tn1) acc.v[tn][h * H + i] = mfma16_i8(fb[tn], fa[i], acc.v[tn][h * H + i]);
+      };
+      i32x4 lo[H], hi[H], fb[TN];
+      read_a(0, 0, 0, lo);
+      read_b(0, 0, fb);
+      for (int it = 0; it < nk; ++it) {
+        const int st = it % S;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          read_a(st, ks, 1, hi);
+          mma(lo, fb, 0, 0, TN);
+          interleave_reads<H, H * TN>();
+          i32x4 nlo[H], nfb[TN];
+          if (ks + 1 < KS) {
+            read_a(st, ks + 1, 0, nlo);
+            read_b(st, ks + 1, nfb);
+            mma(hi, fb, 1, 0, TN);
+            interleave_reads<H + TN, H * TN>();
+          } else {
+            // as below: half of the last MFMAs before the wait for the next stage, half behind it
+            mma(hi, fb, 1, 0, TN / 2);
+            if (AHEAD == 0 || w < HALF) wait_vmcnt<2 * Cfg::LPW * (S - 2)>();
+            if (u.kb + it + 1 == ktail) trim((it + 1) % S, ktail);
+            lds_barrier();
+            issue(st, u.kb + it + S);
+            read_a((it + 1) % S, 0, 0, nlo);
+            read_b((it + 1) % S, 0, nfb);
+            mma(hi, fb, 1, TN / 2, TN);
+            interleave_reads<H + TN, H*(TN - TN / 2)>();
+          }
+#pragma unroll
+          for (int i = 0; i < H; ++i) lo[i] = nlo[i];
+#pragma unroll
+          for (int i = 0; i < TN; ++i) fb[i] = nfb[i];
+        }
+      }
+    } else {
     // MFMA operand fragments of one k-step, read from LDS.
     const int orow = l & 31, ohalf = l >> 5;
     struct Frags {
@@ -407,20 +517,6 @@ struct Tile {
             acc.v[tn][tm] = mfma_i8(f.b[tn][0], f.a[tm][0], acc.v[tn][tm]);
         }
     };
-
-#pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) acc.v[tn][tm] = AccV{};
-
-    const int nk = u.ke - u.kb;
-    constexpr int S = Cfg::STAGES, KS = Cfg::KSTEPS;
-    // Prologue: fill all S stages, wait for the first.
-#pragma unroll
-    for (int st = 0; st < S; ++st) issue(st, u.kb + st);
-    wait_vmcnt<2 * Cfg::LPW * (S - 1)>();  // the loading waves hold 2 LPW loads per stage
-    if (u.kb == ktail) trim(0, ktail);
-    lds_barrier();
     Frags cur;
     read_frags(0, 0, cur);
     for (int it = 0; it < nk; ++it) {
@@ -449,6 +545,7 @@ struct Tile {
         }
         cur = nxt;
       }
+    }
     }
     // The last k-steps issued loads for k-tiles past the unit (out-of-range
     // offsets, which still write zeros into the ring). The compiler does not
@@ -486,14 +583,14 @@ struct Tile {
     float sa[TM];
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
-      const int m = u.m0 + wm * Cfg::WTM + tm * 32 + (l & 31);
+      const int m = u.m0 + wm * Cfg::WTM + row_of(tm, l);
       sa[tm] = m < u.m_end ? ((const float*)a.U)[(int64_t)m * a.ldu] : 0.f;
     }
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int n = u.n0 + wn * Cfg::WTN + tn * 32 + 8 * (i / 4) + 4 * (l >> 5) + i % 4;
+      for (int i = 0; i < 4 * G; ++i) {
+        const int n = u.n0 + wn * Cfg::WTN + col_of(tn, i / 4, l) + i % 4;
         const float sb = n < a.N ? vb[(int64_t)n * a.ldv] : 0.f;
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) {
@@ -518,19 +615,19 @@ struct Tile {
     const bool bf = a.d_type == DT_BF16;
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
-      const int row = tm * 32 + (l & 31);
+      const int row = row_of(tm, l);
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < G; ++g) {
           uint16_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float x = a.alpha * value(acc, tn, tm, 4 * g + j);
             h[j] = bf ? f32_to_bf16_bits(x) : f32_to_f16_bits(x);
           }
-          const int ch = tn * 4 + g;
-          *(u16x4*)(st + row * WROWB + ((ch ^ swz<WCH>(row)) << 4) + 8 * (l >> 5)) = u16x4{h[0], h[1], h[2], h[3]};
+          const int col = col_of(tn, g, l);
+          *(u16x4*)(st + row * WROWB + (((col / 8) ^ swz<WCH>(row)) << 4) + 8 * (col / 4 % 2)) = u16x4{h[0], h[1], h[2], h[3]};
         }
     }
     __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's LDS writes are done (lgkmcnt 0)
@@ -567,7 +664,7 @@ struct Tile {
     if (scaled) scale_sums(a, u, acc);
     if constexpr (STAGED) {
       if (plain16(a) && (!Cfg::INT || scaled)) {
-        store_staged(a, u, acc, smem);
+        store_staged<!Cfg::INT>(a, u, acc, smem);
         return;
       }
     }
@@ -577,6 +674,37 @@ struct Tile {
         each4(a, u, [&](int m, int n, int tn, int tm, int g) {
           epi_store4(a, 0, m, n, S4{acc.v[tn][tm][4 * g], acc.v[tn][tm][4 * g + 1], acc.v[tn][tm][4 * g + 2], acc.v[tn][tm][4 * g + 3]});
         });
+        return;
+      }
+    }
+    if constexpr (Cfg::INT) {
+      if (a.c_type >= 0 && a.beta != 0.f) {
+        // a block row's C is loaded before any of it is stored (D may be C: the compiler keeps each load behind the
+        // stores before it, a latency for every four outputs; 24 experts, 1501 rows, N 1000, K 2075: 38 us so)
+        const int w = wave_id(), l = lane_id();
+        const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm) {
+          const int m = u.m0 + wm * Cfg::WTM + row_of(tm, l);
+          const bool in = m < u.m_end;
+          float c[TN][G][4];
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const int n = u.n0 + wn * Cfg::WTN + col_of(tn, g, l);
+              if (in && n < a.N) load_c4(a, m, n, c[tn][g]);
+            }
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const int n = u.n0 + wn * Cfg::WTN + col_of(tn, g, l);
+              if (in && n < a.N)
+                epi_store4c(a, m, n, f32x4{value(acc, tn, tm, 4 * g), value(acc, tn, tm, 4 * g + 1), value(acc, tn, tm, 4 * g + 2), value(acc, tn, tm, 4 * g + 3)},
+                            f32x4{c[tn][g][0], c[tn][g][1], c[tn][g][2], c[tn][g][3]});
+            }
+        }
         return;
       }
     }
@@ -593,13 +721,13 @@ struct Tile {
     const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
-      const int m = u.m0 + wm * Cfg::WTM + tm * 32 + (l & 31);
+      const int m = u.m0 + wm * Cfg::WTM + row_of(tm, l);
       if (m >= u.m_end) continue;
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int n = u.n0 + wn * Cfg::WTN + tn * 32 + 8 * g + 4 * (l >> 5);
+        for (int g = 0; g < G; ++g) {
+          const int n = u.n0 + wn * Cfg::WTN + col_of(tn, g, l);
           if (n < a.N) f(m, n, tn, tm, g);
         }
     }
@@ -621,14 +749,14 @@ struct Tile {
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int q = (tn * TM + tm) * 4 + g;
+        for (int g = 0; g < G; ++g) {
+          const int q = (tn * TM + tm) * G + g;
           S4 v = {acc.v[tn][tm][4 * g], acc.v[tn][tm][4 * g + 1], acc.v[tn][tm][4 * g + 2], acc.v[tn][tm][4 * g + 3]};
           store_sc1_x4(r, base + q * 1024, __builtin_bit_cast(i32x4, v));
         }
   }
 
-  // Chunk c = (tn * TM + tm) * 4 + g of a lane's partial tile: accumulator
+  // Chunk c = (tn * TM + tm) * G + g of a lane's partial tile: accumulator
   // elements 4g .. 4g+3 of block (tn, tm), stored at base + 1024 c.
   static constexpr int NCH = NQ;
   __device__ __forceinline__ static bool holds_partial() { return true; }
@@ -636,11 +764,11 @@ struct Tile {
     return (uint32_t)((wave_id() * NQ * 64 + lane_id()) * 16 + c * 1024);
   }
   __device__ __forceinline__ static S4 get4(const Acc& acc, int c) {
-    const int tn = c / (TM * 4), tm = (c / 4) % TM, g = c % 4;
+    const int tn = c / (TM * G), tm = (c / G) % TM, g = c % G;
     return S4{acc.v[tn][tm][4 * g], acc.v[tn][tm][4 * g + 1], acc.v[tn][tm][4 * g + 2], acc.v[tn][tm][4 * g + 3]};
   }
   __device__ __forceinline__ static void set4(Acc& acc, int c, const S4& x) {
-    const int tn = c / (TM * 4), tm = (c / 4) % TM, g = c % 4;
+    const int tn = c / (TM * G), tm = (c / G) % TM, g = c % G;
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc.v[tn][tm][4 * g + j] = x[j];
   }
