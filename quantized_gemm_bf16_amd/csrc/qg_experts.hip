@@ -35,23 +35,43 @@ __device__ __forceinline__ int entry(const GroupArgs& a, int i) {
   return e >= 0 && e < a.E ? e : -1;
 }
 
+constexpr int kHeld = 4;  // entries that a lane has loaded ahead
+
+// f(i, e) for the entries i of the wave's run [i0, i1), 64 at a time (e < 0: nobody's, or i past the run), by whole waves
+template <class F>
+__device__ __forceinline__ void each64(const GroupArgs& a, int i0, int i1, F f) {
+  const int l = lane_id();
+  for (int i = i0; i < i1; i += 64 * kHeld) {
+    int e[kHeld];
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) e[j] = i + 64 * j + l < i1 ? entry(a, i + 64 * j + l) : -1;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (i + 64 * j < i1) f(i + 64 * j + l, e[j]);
+  }
+}
+
 // Counts of the workgroup's range, a table of E per wave.
-__device__ __forceinline__ void count_range(const GroupArgs& a, int (*hist)[kSortExperts], int c0, int c1) {
-  const int w = wave_id(), per = a.chunk / kSortWaves;
+__device__ __forceinline__ void count_range(const GroupArgs& a, int (*hist)[kSortExperts], int i0, int i1) {
+  const int w = wave_id();
   for (int i = threadIdx.x; i < kSortWaves * kSortExperts; i += kSortThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  const int i0 = c0 + w * per, i1 = min(c1, i0 + per);
-  for (int i = i0 + lane_id(); i < i1; i += 64) {
-    const int e = entry(a, i);
+  each64(a, i0, i1, [&](int, int e) {
     if (e >= 0) atomicAdd(&hist[w][e], 1);
-  }
+  });
   __syncthreads();
+}
+__device__ __forceinline__ void wave_run(const GroupArgs& a, int& i0, int& i1) {
+  const int c0 = blockIdx.x * a.chunk, per = a.chunk / kSortWaves;
+  i0 = c0 + wave_id() * per;
+  i1 = min(min(a.n, c0 + a.chunk), i0 + per);
 }
 
 __global__ __launch_bounds__(kSortThreads) void group_count_kernel(const GroupArgs a) {
   __shared__ int hist[kSortWaves][kSortExperts];
-  const int c0 = blockIdx.x * a.chunk;
-  count_range(a, hist, c0, min(a.n, c0 + a.chunk));
+  int i0, i1;
+  wave_run(a, i0, i1);
+  count_range(a, hist, i0, i1);
   for (int e = threadIdx.x; e < a.E; e += kSortThreads) {
     int sum = 0;
 #pragma unroll
@@ -62,30 +82,41 @@ __global__ __launch_bounds__(kSortThreads) void group_count_kernel(const GroupAr
 
 __global__ __launch_bounds__(kSortThreads) void group_place_kernel(const GroupArgs a) {
   __shared__ int hist[kSortWaves][kSortExperts];
+  __shared__ int all[kSortExperts], before[kSortExperts];
   __shared__ int wave_total[kSortWaves], grand;
-  const int c = blockIdx.x, c0 = c * a.chunk, c1 = min(a.n, c0 + a.chunk);
-  const int w = wave_id(), l = lane_id();
-  count_range(a, hist, c0, c1);
-  // thread t: experts 2 t and 2 t + 1 (kSortExperts = 2 kSortThreads)
-  int all[2], before[2];
+  const int c = blockIdx.x, w = wave_id(), l = lane_id();
+  int i0, i1;
+  wave_run(a, i0, i1);
+  count_range(a, hist, i0, i1);
+  if (a.chunks == 1) {
+    for (int e = threadIdx.x; e < kSortExperts; e += kSortThreads) {
+      int sum = 0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int e = 2 * threadIdx.x + j;
-    all[j] = before[j] = 0;
-    if (e >= a.E) continue;
-    if (a.chunks > 1) {
-      for (int q = 0; q < a.chunks; ++q) {
+      for (int q = 0; q < kSortWaves; ++q) sum += hist[q][e];
+      all[e] = sum;
+      before[e] = 0;
+    }
+  } else {
+    // the columns of the table of counts: `parts` threads share one where the experts are few
+    for (int e = threadIdx.x; e < kSortExperts; e += kSortThreads) all[e] = before[e] = 0;
+    __syncthreads();
+    const int width = (a.E + 63) & ~63, parts = max(1, kSortThreads / width);
+    for (int e = threadIdx.x % width, p = threadIdx.x / width; p < parts && e < a.E; e += kSortThreads) {
+      int sum = 0, low = 0;
+#pragma unroll 16
+      for (int q = p; q < a.chunks; q += parts) {
         const int x = a.counts[(int64_t)q * a.E + e];
-        all[j] += x;
-        before[j] += q < c ? x : 0;
+        sum += x;
+        low += q < c ? x : 0;
       }
-    } else {
-#pragma unroll
-      for (int q = 0; q < kSortWaves; ++q) all[j] += hist[q][e];
+      atomicAdd(&all[e], sum);
+      atomicAdd(&before[e], low);
     }
   }
-  // exclusive prefix of `all` over the experts
-  int incl = all[0] + all[1];
+  __syncthreads();
+  // Exclusive prefix over the experts; thread t has 2 t and 2 t + 1 (kSortExperts = 2 kSortThreads).
+  const int n0 = all[2 * threadIdx.x], n1 = all[2 * threadIdx.x + 1];
+  int incl = n0 + n1;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int y = __shfl_up(incl, d, 64);
@@ -93,16 +124,15 @@ __global__ __launch_bounds__(kSortThreads) void group_place_kernel(const GroupAr
   }
   if (l == 63) wave_total[w] = incl;
   __syncthreads();
-  int at = incl - all[0] - all[1];
+  int at = incl - n0 - n1;
   for (int q = 0; q < w; ++q) at += wave_total[q];
-  if (threadIdx.x == kSortThreads - 1) grand = at + all[0] + all[1];
+  if (threadIdx.x == kSortThreads - 1) grand = at + n0 + n1;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * threadIdx.x + j;
     if (c == 0 && e <= a.E) a.offsets[e] = at;
-    int place = at + before[j];
-    at += all[j];
-    if (e >= a.E) continue;
+    int place = at + before[e];
+    at += j ? n1 : n0;
 #pragma unroll
     for (int q = 0; q < kSortWaves; ++q) {
       const int x = hist[q][e];
@@ -111,10 +141,7 @@ __global__ __launch_bounds__(kSortThreads) void group_place_kernel(const GroupAr
     }
   }
   __syncthreads();
-  const int per = a.chunk / kSortWaves, i0 = c0 + w * per, i1 = min(c1, i0 + per);
-  for (int i = i0; i < i1; i += 64) {
-    const bool in = i + l < i1;
-    const int e = in ? entry(a, i + l) : -1;
+  each64(a, i0, i1, [&](int i, int e) {
     uint64_t same = __ballot(e >= 0);
     for (int b = 1; b < a.E; b <<= 1) {
       const uint64_t set = __ballot((e & b) != 0);
@@ -125,9 +152,9 @@ __global__ __launch_bounds__(kSortThreads) void group_place_kernel(const GroupAr
     __builtin_amdgcn_wave_barrier();
     if (e >= 0 && __ffsll((unsigned long long)same) - 1 == l) lds_set(&hist[w][e], pos + __popcll(same));
     __builtin_amdgcn_wave_barrier();
-    if (in) a.back[i + l] = pos;
-    if (e >= 0) a.rows[pos] = (i + l) / a.K;
-  }
+    if (i < i1) a.back[i] = pos;
+    if (e >= 0) a.rows[pos] = i / a.K;
+  });
   // rows behind the last expert's come from nowhere
   for (int i = grand + c * kSortThreads + threadIdx.x; i < a.n; i += a.chunks * kSortThreads) a.rows[i] = -1;
 }

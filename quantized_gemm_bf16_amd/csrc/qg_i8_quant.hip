@@ -29,7 +29,7 @@ namespace {
 
 // Element k of y in 64 bits, from memory.
 template <int DT, bool GATED>
-__device__ __attribute__((noinline)) double value64(const char* row, int K, int k) {
+__device__ __forceinline__ double value64(const char* row, int K, int k) {
   const auto get = [&](int64_t i) -> double {
     if constexpr (DT == DT_F32) return ((const float*)row)[i];
     const uint16_t h = ((const uint16_t*)row)[i];
@@ -57,7 +57,7 @@ __device__ __forceinline__ double lanes_max(double x) {
 // L lanes (a part of a wave, or whole waves: the workgroup) take one row,
 // U units of 8 elements each.
 template <int DT, bool GATED, int L, int U>
-__global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quantize_kernel(const I8QuantArgs a) {
+__global__ __launch_bounds__(L < 256 ? 256 : L, GATED && L == 512 ? 4 : 1) void i8_quantize_kernel(const I8QuantArgs a) {
   constexpr int NT = L < 256 ? 256 : L, RPB = NT / L, LW = L < 64 ? L : 64, NW = L / 64;
   __shared__ uint32_t wave_top[L > 64 ? NW : 1];
   __shared__ double wave_top64[L > 64 ? NW : 1];
@@ -68,11 +68,20 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quantize_kernel(const I8
   if (a.rows && live) src = a.rows[row];
   const bool there = live && src >= 0 && src < a.T;
   const char* x = (const char*)a.X + (there ? src : 0) * (int64_t)a.ldx * Raw<DT>::ES;
-  float v[U][8];
-  uint32_t deep[U];  // elements that need 64 bits whatever their neighbours (bit per element)
-  uint32_t top = 0;
+  // what is held of a row: its elements as loaded, or y in fp32 with each unit's lowest gate
+  Raw<DT> in[U];
+  float v[GATED ? U : 1][8], low[GATED ? U : 1];
+  uint32_t most[U], top = 0;  // largest |y| of a unit, of the row (as bits: a NaN is more than everything)
+  static_assert(U <= 8, "a bit per element");
+  // the element of the lowest bit of `todo`, which is cleared: bit 8 i + j is the lane's unit i, element j
+  const auto element = [&](uint64_t& todo) {
+    const int b = __builtin_ctzll(todo);
+    todo &= todo - 1;
+    return ((b >> 3) * L + l) * 8 + (b & 7);
+  };
+  const auto val = [&](int i, int j) { return GATED ? v[GATED ? i : 0][j] : in[i].at(j); };
   {
-    Raw<DT> in[U], up[GATED ? U : 1];
+    Raw<DT> up[GATED ? U : 1];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int k = (i * L + l) * 8, n = there ? a.K - k : 0;
@@ -81,20 +90,21 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quantize_kernel(const I8
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      deep[i] = 0;
+      if constexpr (GATED) {
+        low[i] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = in[i].at(j);
-        if constexpr (GATED) {
-          const float g = v[i][j];
+        for (int j = 0; j < 8; ++j) {
+          const float g = in[i].at(j);
           v[i][j] = g * up[i].at(j) * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504f));
-          deep[i] |= (g < -32.f ? 1u : 0u) << j | (g < -8.f ? 1u : 0u) << (8 + j);
+          low[i] = fminf(low[i], g);
         }
-        top = max(top, __builtin_bit_cast(uint32_t, v[i][j]) & 0x7FFFFFFFu);
       }
+      most[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most[i] = max(most[i], __builtin_bit_cast(uint32_t, val(i, j)) & 0x7FFFFFFFu);
+      top = max(top, most[i]);
     }
   }
-  // the row's largest |v|, as bits (a NaN is more than everything)
   top = lanes_max<LW>(top);
   if constexpr (L > 64) {
     if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = top;
@@ -105,25 +115,27 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quantize_kernel(const I8
   const bool slow = top >= 0x7F800000u || (top != 0 && top < 0x21800000u);  // not finite, or under 2^-60
   double amax = __builtin_bit_cast(float, top);
   if constexpr (GATED) {
-    // in 64 bits over the candidates
-    const float near = slow ? 0.f : __builtin_bit_cast(float, top) * (1.f - 0x1p-16f);
-    double m = 0;
-    bool bad = false;
+    // in 64 bits over the elements that may be the largest
+    const uint32_t near = slow ? 0u : top == 0 ? ~0u : __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, top) * (1.f - 0x1p-16f));
+    uint64_t todo = 0;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      uint32_t todo = deep[i] & 0xFF;
+      uint32_t bits = low[i] < -32.f ? 0xFF : 0;
+      if (most[i] >= near) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (slow || (top != 0 && fabsf(v[i][j]) >= near)) todo |= 1u << j;
-      const int k = (i * L + l) * 8, n = there ? a.K - k : 0;
-      if (n < 8) todo &= n > 0 ? (1u << n) - 1 : 0;
-      while (todo) {
-        const int j = __builtin_ctz(todo);
-        todo &= todo - 1;
-        const double y = fabs(value64<DT, GATED>(x, a.K, k + j));
-        bad |= !(y <= 1.7976931348623157e308);
-        m = fmax(m, y);
+        for (int j = 0; j < 8; ++j)
+          if ((__builtin_bit_cast(uint32_t, v[i][j]) & 0x7FFFFFFFu) >= near) bits |= 1u << j;
       }
+      todo |= (uint64_t)bits << (8 * i);
+    }
+    double m = 0;
+    bool bad = false;
+    while (todo) {
+      const int k = element(todo);
+      if (!there || k >= a.K) continue;
+      const double y = fabs(value64<DT, GATED>(x, a.K, k));
+      bad |= !(y <= 1.7976931348623157e308);
+      m = fmax(m, y);
     }
     if (bad) m = __builtin_bit_cast(double, (uint64_t)0x7FF << 52);
     m = lanes_max<LW>(m);
@@ -142,39 +154,48 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quantize_kernel(const I8
   const bool zero = none || s == 0.f;
   const float inv = zero ? 0.f : (float)(1.0 / (double)s);
   if (live && l == 0) a.S[row * a.lds] = s;
+  uint64_t todo = 0;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int k = (i * L + l) * 8, n = live ? a.K - k : 0;
-    uint32_t lo = 0, hi = 0, todo = 0;
+    // a code is the low byte of t + 1.5 * 2^23, which rounds t to an integer (ties to even)
+    constexpr float kRound = 12582912.f;
+    const float off = !GATED ? 0x1p-22f : low[GATED ? i : 0] < -8.f ? 0x1p-17f : 0x1p-19f;
+    uint32_t c[8], q[2];
+    float worst = 0.f;
+    const auto doubt = [&](int j, uint32_t& code) {
+      const float t = val(i, j) * inv, r = t + kRound;
+      code = __builtin_bit_cast(uint32_t, r);
+      return __builtin_fmaf(fabsf(t), off, fabsf(t - (r - kRound)));
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float t = v[i][j] * inv, q = rintf(t);
-      const float off = !GATED ? 0x1p-22f : (deep[i] >> (8 + j) & 1) ? 0x1p-17f : 0x1p-19f;
-      if (__builtin_fmaf(fabsf(t), off, fabsf(t - q)) >= 0.5f) todo |= 1u << j;
-      const uint32_t c = (uint32_t)(int)q & 0xFF;
-      (j < 4 ? lo : hi) |= c << (8 * (j & 3));
+    for (int j = 0; j < 8; ++j) worst = fmaxf(worst, doubt(j, c[j]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      q[h] = zero ? 0
+                  : __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x0C0C0400u),
+                                          __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0C0C0400u), 0x05040100u);
+    uint32_t bits = slow || (GATED && low[GATED ? i : 0] < -32.f) ? 0xFF : 0;
+    if (worst >= 0.5f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (doubt(j, c[j]) >= 0.5f) bits |= 1u << j;
     }
-    todo |= slow ? 0xFF : deep[i] & 0xFF;
-    if (zero || !there) todo = lo = hi = 0;
-    if (n < 8) todo &= n > 0 ? (1u << n) - 1 : 0;
-    while (todo) {
-      const int j = __builtin_ctz(todo);
-      todo &= todo - 1;
-      const double q = fmin(fmax(rint(value64<DT, GATED>(x, a.K, k + j) / (double)s), -127.0), 127.0);
-      const uint32_t c = (uint32_t)(int)q & 0xFF, at = 8 * (j & 3), keep = ~(0xFFu << at);
-      if (j < 4)
-        lo = (lo & keep) | c << at;
-      else
-        hi = (hi & keep) | c << at;
-    }
-    char* q = a.Q + row * a.ldq + k;
+    todo |= (uint64_t)bits << (8 * i);
+    char* p = a.Q + row * a.ldq + k;
     if (n >= 8) {
-      *(uint64_t*)q = (uint64_t)hi << 32 | lo;
+      *(uint64_t*)p = (uint64_t)q[1] << 32 | q[0];
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) q[j] = (char)((j < 4 ? lo : hi) >> (8 * (j & 3)));
+        if (j < n) p[j] = (char)(q[j / 4] >> (8 * (j & 3)));
     }
+  }
+  // the codes in doubt again, over those that just went out
+  if (zero || !there) todo = 0;
+  while (todo) {
+    const int k = element(todo);
+    if (k < a.K) a.Q[row * a.ldq + k] = (char)(int)fmin(fmax(rint(value64<DT, GATED>(x, a.K, k) / (double)s), -127.0), 127.0);
   }
 }
 
@@ -238,6 +259,10 @@ hipError_t quantize_lu(const I8QuantArgs& a, hipStream_t s) {
   return launch_parts(i8_quantize_kernel<DT, GATED, L, U>, a, most, (int64_t)a.ldx * Raw<DT>::ES, NT, RPB, 1, s);
 }
 
+// Lanes per row and units per lane, so that a row just fits: a lane of one wave has up to four units, of several up to four
+// too, of 1024 lanes eight. bf16, 8192 rows gated: K 14336 139 us with 512 lanes of four units (two such workgroups per
+// CU), 168 with 256 of eight, 193 with 1024 of two; K 7168 58 with 256 of four. 32768 rows gathered, K 7168: 107 with 256 of
+// four, 133 with one wave of 16, 112 with two of eight; 125 with the next row's loads ahead of this one's work.
 template <int DT, bool GATED>
 hipError_t quantize_t(const I8QuantArgs& a, hipStream_t s) {
   if (a.cpr <= 8) return quantize_lu<DT, GATED, 8, 1>(a, s);
@@ -248,7 +273,8 @@ hipError_t quantize_t(const I8QuantArgs& a, hipStream_t s) {
   if (a.cpr <= 256) return quantize_lu<DT, GATED, 64, 4>(a, s);
   if (a.cpr <= 512) return quantize_lu<DT, GATED, 256, 2>(a, s);
   if (a.cpr <= 1024) return quantize_lu<DT, GATED, 256, 4>(a, s);
-  if (a.cpr <= 2048) return quantize_lu<DT, GATED, 256, 8>(a, s);
+  if (a.cpr <= 2048) return quantize_lu<DT, GATED, 512, 4>(a, s);
+  if (a.cpr <= 4096) return quantize_lu<DT, GATED, 1024, 4>(a, s);
   return quantize_lu<DT, GATED, 1024, 8>(a, s);
 }
 
