@@ -212,26 +212,25 @@ def routing(score=ROUTE_SOFTMAX, top_k=1, groups=1, top_groups=1, group_best=1, 
                    float(scale), 0)
 
 
+def _ptr(t):
+    """Device address of a tensor; a raw address or None as it is."""
+    if t is None or t.__class__ is int:
+        return t
+    return t.data_ptr()
+
+
+# What a call without a layout for an operand reads has to be a contiguous tensor of the type, of `n` elements at least; one
+# with a layout has to be of the type (None and raw addresses are the caller's word).
 def _bad_table(t, dtype, n=0):
-    """A status where `t` is a tensor that is not what a call without a layout for it reads: `dtype`, contiguous, n
-    elements at least (raw pointers and None are the caller's word)."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return OK
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         return ERR_UNSUPPORTED
     return OK if t.is_contiguous() and t.numel() >= n else ERR_INVALID_ARG
 
 
 def _bad_type(t, dtype):
-    return ERR_UNSUPPORTED if not (t is None or isinstance(t, int)) and t.dtype != dtype else OK
-
-
-def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return OK if t is None or t.__class__ is int or t.dtype is dtype else ERR_UNSUPPORTED
 
 
 def _check(st, what):

@@ -507,15 +507,15 @@ int route_args(const qg_routing* r, const void* X, const qg_layout* Xd, const fl
   a.bias = bias;
   a.ids = ids;
   a.W = W;
-  a.T = Xd->rows;
+  a.T = (int32_t)Xd->rows;
   a.ldx = (int32_t)Xd->ld;
   a.ldi = (int32_t)Id->ld;
   a.ldw = (int32_t)Wd->ld;
-  a.K = r->top_k;
-  a.groups = groups;
-  a.per = (int32_t)per;
-  a.kept = kept;
-  a.shift = shift;
+  a.K = (int8_t)r->top_k;
+  a.groups = (int8_t)groups;
+  a.per = (int16_t)per;
+  a.kept = (int8_t)kept;
+  a.shift = (int8_t)shift;
   a.flags = (r->score == QG_ROUTE_SIGMOID ? ROUTE_SIGMOID : 0) | (groups > 1 && r->group_best == 2 ? ROUTE_BEST2 : 0) |
             (r->renormalize ? ROUTE_RENORM : 0);
   a.scale = r->scale;
@@ -1280,12 +1280,12 @@ int qg_group_rows(qg_handle* h, int experts, const int32_t* ids, const qg_layout
   a.K = (int32_t)Idesc->cols;
   a.ldi = (int32_t)Idesc->ld;
   a.E = experts;
-  group_chunks(n, &a.chunk, &a.chunks);
-  if (a.chunks > 1) {
-    if (!ws || !ws->partials || ws->partials_size < (size_t)a.chunks * experts * 4) return QG_ERR_WORKSPACE;
-    if (!aligned16(ws->partials)) return QG_ERR_ALIGNMENT;
-    a.counts = (int32_t*)ws->partials;
-  }
+  // 256 ranges at most, whose counts go through the workspace
+  const bool space = ws && ws->partials && ws->partials_size >= (size_t)experts * 1024;
+  if (n > kGroupAlone && !space) return QG_ERR_WORKSPACE;
+  if (space && !aligned16(ws->partials)) return QG_ERR_ALIGNMENT;
+  group_chunks(n, space, &a.chunk, &a.chunks);
+  if (a.chunks > 1) a.counts = (int32_t*)ws->partials;
   if (!h->online) return QG_ERR_HIP;
   return launch_group(a, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
@@ -1302,7 +1302,7 @@ int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_
     return st;
   if (T > 0 && K > 0 && !back) return QG_ERR_INVALID_ARG;
   if (!aligned4(back)) return QG_ERR_ALIGNMENT;
-  CombineArgs a{};
+  CombineAddArgs a{};
   if (beta != 0.f) {
     if (!Cdesc) return QG_ERR_INVALID_ARG;
     if ((st = check_layout(Cdesc))) return st;
@@ -1310,6 +1310,7 @@ int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_
     if ((st = check_table(C, Cdesc, T, H))) return st;
     a.C = C;
     a.ldc = (int32_t)Cdesc->ld;
+    a.c_type = Cdesc->type;
   }
   if (T == 0 || H == 0) return QG_OK;
   a.R = R;
@@ -1323,10 +1324,9 @@ int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_
   a.K = (int32_t)K;
   a.N = (int32_t)Rdesc->rows;
   a.H = (int32_t)H;
-  a.cpr = (int32_t)cdiv(H, 8);
   a.beta = beta;
   if (!h->online) return QG_ERR_HIP;
-  return launch_combine(a, Rdesc->type, beta != 0.f ? Cdesc->type : -1, Ydesc->type, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+  return launch_combine(a, Rdesc->type, Ydesc->type, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_plan(qg_handle* h, const qg_operation* op, const qg_layout* Adesc, const qg_layout* Udesc,

@@ -87,30 +87,69 @@ __device__ __forceinline__ float logit(const RouteArgs& a, int64_t t, int e) {
   return DT == DT_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
 }
 
-// The `rounds` best keys (0: not there): lane r gets the expert of the r-th, -1 where fewer are there.
+// The `rounds` best keys (0: not there): lane r gets the expert of the r-th, -1 where fewer are there. Few keys per
+// lane are put in order first (`tag` holds a byte for each, its place in the lane), so that a round looks at the
+// lanes' first keys only and the winner's others move up.
 template <class Key, int NV>
 __device__ __forceinline__ int choose(Key (&key)[NV], int e0, int rounds, int& found) {
+  constexpr bool kSorted = NV <= 4;
   const int lane = lane_id();
+  uint32_t tag = 0;
+  if constexpr (kSorted) {
+    uint32_t at[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) at[j] = j;
+    const auto order = [&](int i, int j) {  // equal keys stay as they are: i is before j
+      const bool swap = key[j] > key[i];
+      const Key k = swap ? key[j] : key[i];
+      key[j] = swap ? key[i] : key[j];
+      key[i] = k;
+      const uint32_t t = swap ? at[j] : at[i];
+      at[j] = swap ? at[i] : at[j];
+      at[i] = t;
+    };
+    // (neighbours only, so that no key passes an equal one)
+#pragma unroll
+    for (int n = NV - 1; n > 0; --n)
+#pragma unroll
+      for (int j = 0; j < n; ++j) order(j, j + 1);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) tag |= at[j] << (8 * j);
+  }
   int mine = -1;
   found = 0;
   for (int r = 0; r < rounds; ++r) {
     Key top = key[0];
+    if constexpr (!kSorted) {
 #pragma unroll
-    for (int j = 1; j < NV; ++j) top = max(top, key[j]);
+      for (int j = 1; j < NV; ++j) top = max(top, key[j]);
+    }
     top = wave_max(top);
     if (top == 0) break;
-    uint64_t at[NV], any = 0;
+    int w, e;
+    if constexpr (kSorted) {
+      w = __builtin_ctzll(__ballot(key[0] == top));
+      e = __builtin_amdgcn_readlane(e0, w) + (__builtin_amdgcn_readlane((int)tag, w) & 0xFF);
+      if (lane == w) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) any |= at[j] = __ballot(key[j] == top);
-    const int w = __builtin_ctzll(any);
-    int first = NV - 1;
+        for (int j = 0; j + 1 < NV; ++j) key[j] = key[j + 1];
+        key[NV - 1] = 0;
+        tag >>= 8;
+      }
+    } else {
+      uint64_t at[NV], any = 0;
 #pragma unroll
-    for (int j = NV - 2; j >= 0; --j)
-      if (at[j] >> w & 1) first = j;
-    const int e = __builtin_amdgcn_readlane(e0, w) + first;
+      for (int j = 0; j < NV; ++j) any |= at[j] = __ballot(key[j] == top);
+      w = __builtin_ctzll(any);
+      int first = NV - 1;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (lane == w && j == first) key[j] = 0;
+      for (int j = NV - 2; j >= 0; --j)
+        if (at[j] >> w & 1) first = j;
+      e = __builtin_amdgcn_readlane(e0, w) + first;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (lane == w && j == first) key[j] = 0;
+    }
     if (lane == r) mine = e;
     ++found;
   }
@@ -130,40 +169,35 @@ __device__ __forceinline__ F standing(F b1, F b2, int shift, bool best2) {
   return best2 && b2 > (F)kMinusInf ? b1 + b2 : b1;
 }
 
-// The choice in 64 bits.
+// The choice in 64 bits. Logits are read again where they are needed: this seldom runs, and its registers are the kernel's.
 template <int DT, int NV>
-__device__ __attribute__((noinline)) int choose64(const RouteArgs& a, int64_t t, int e0, int count, int& found) {
-  double p[NV], x[NV];
-  double m = kMinusInf;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    x[j] = kMinusInf;
-    if (j < count) x[j] = logit<DT>(a, t, e0 + j);
-    if (!(x[j] > kMinusInf)) x[j] = kMinusInf;
-    m = x[j] > m ? x[j] : m;
+__device__ __attribute__((noinline)) int choose64(const RouteArgs a, int64_t t, int e0, int count, int& found) {
+  const auto get = [&](int j) -> double {
+    const double x = j < count ? logit<DT>(a, t, e0 + j) : kMinusInf;
+    return x > kMinusInf ? x : (double)kMinusInf;
+  };
+  double m = kMinusInf, sum = 1;
+  if (!(a.flags & ROUTE_SIGMOID)) {
+    for (int j = 0; j < count; ++j) m = fmax(m, get(j));
+    for (int d = 1; d < 64; d <<= 1) m = fmax(m, __shfl_xor(m, d, 64));
   }
-  if (a.flags & ROUTE_SIGMOID) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) p[j] = 1.0 / (1.0 + exp(-x[j]));
-  } else {
-    for (int d = 1; d < 64; d <<= 1) {
-      const double o = __shfl_xor(m, d, 64);
-      m = o > m ? o : m;
-    }
-    double sum = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) sum += p[j] = !(x[j] > kMinusInf) ? 0.0 : x[j] == m ? 1.0 : exp(x[j] - m);
+  const auto score = [&](double x) -> double {
+    if (a.flags & ROUTE_SIGMOID) return 1.0 / (1.0 + exp(-x));
+    return !(x > kMinusInf) ? 0.0 : x == m ? 1.0 : exp(x - m);
+  };
+  if (!(a.flags & ROUTE_SIGMOID)) {
+    sum = 0;
+    for (int j = 0; j < count; ++j) sum += score(get(j));
     sum = wave_sum(sum);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) p[j] /= sum;
   }
   uint64_t key[NV];
   double b1 = kMinusInf, b2 = kMinusInf;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    double s = p[j], k = x[j];
+    const double x = get(j);
+    double s = score(x) / sum, k = x;
     if (a.bias && j < count) k = s += a.bias[e0 + j];
-    const bool there = x[j] > kMinusInf && k > kMinusInf;
+    const bool there = x > kMinusInf && k > kMinusInf;
     key[j] = there ? ordered(k) : 0;
     if (!(a.flags & ROUTE_BEST2)) s = k;
     if (!there) s = kMinusInf;
