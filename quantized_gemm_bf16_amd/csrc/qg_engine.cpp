@@ -1257,7 +1257,7 @@ int qg_route(qg_handle* h, const qg_routing* routing, const void* X, const qg_la
   if (st != QG_OK) return st;
   if (Xdesc->rows == 0) return QG_OK;
   if (!h->online) return QG_ERR_HIP;
-  return launch_route(a, Xdesc->type, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
+  return launch_route(a, Xdesc->type, h->cus, stream) == hipSuccess ? QG_OK : QG_ERR_HIP;
 }
 
 int qg_group_rows(qg_handle* h, int experts, const int32_t* ids, const qg_layout* Idesc, int32_t* offsets, int32_t* rows,

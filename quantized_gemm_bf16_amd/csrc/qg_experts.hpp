@@ -54,7 +54,7 @@ struct CombineAddArgs : CombineArgs {
   float beta;
 };
 
-hipError_t launch_route(const RouteArgs& a, int x_type, hipStream_t s);
+hipError_t launch_route(const RouteArgs& a, int x_type, int cus, hipStream_t s);
 // Entries of one workgroup's range and the number of ranges, for n entries.
 // (workspace: the caller has one for the table of counts)
 void group_chunks(int64_t n, bool workspace, int* chunk, int* chunks);
