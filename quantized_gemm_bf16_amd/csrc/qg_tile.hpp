@@ -20,6 +20,7 @@
 #pragma once
 #include "qg_args.hpp"
 #include "qg_device.hpp"
+#include "qg_rows.hpp"
 #include "qg_sched.hpp"
 
 namespace qg {
@@ -677,34 +678,9 @@ struct Tile {
         return;
       }
     }
-    if constexpr (Cfg::INT) {
-      if (a.c_type >= 0 && a.beta != 0.f) {
-        // a block row's C is loaded before any of it is stored (D may be C: the compiler keeps each load behind the
-        // stores before it, a latency for every four outputs; 24 experts, 1501 rows, N 1000, K 2075: 38 us so)
-        const int w = wave_id(), l = lane_id();
-        const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
-          const int m = u.m0 + wm * Cfg::WTM + row_of(tm, l);
-          const bool in = m < u.m_end;
-          float c[TN][G][4];
-#pragma unroll
-          for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const int n = u.n0 + wn * Cfg::WTN + col_of(tn, g, l);
-              if (in && n < a.N) load_c4(a, m, n, c[tn][g]);
-            }
-#pragma unroll
-          for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-              const int n = u.n0 + wn * Cfg::WTN + col_of(tn, g, l);
-              if (in && n < a.N)
-                epi_store4c(a, m, n, f32x4{value(acc, tn, tm, 4 * g), value(acc, tn, tm, 4 * g + 1), value(acc, tn, tm, 4 * g + 2), value(acc, tn, tm, 4 * g + 3)},
-                            f32x4{c[tn][g][0], c[tn][g][1], c[tn][g][2], c[tn][g][3]});
-            }
-        }
+    if constexpr (Cfg::INT && MB == 32) {
+      if (a.epi == 0) {
+        store_slabs(a, u, acc, smem);
         return;
       }
     }
@@ -712,6 +688,79 @@ struct Tile {
       epi_store4(a, m, n,
                  f32x4{value(acc, tn, tm, 4 * g), value(acc, tn, tm, 4 * g + 1), value(acc, tn, tm, 4 * g + 2), value(acc, tn, tm, 4 * g + 3)});
     });
+  }
+
+  // w8a8 results of the small tiles that read C or are fp32: a block row of a wave's tile at a time goes through LDS in
+  // fp32, so that C is read and D written as whole row segments (in place too: a lane reads what it writes, before it).
+  // 16-byte chunks are under the XOR key of the operand ring. 24 experts, 1501 rows, N 1000, K 2075, C fp16: 29.4 us, 32.7
+  // with four columns per lane and access; the next block row's C ahead of this one's work 28.7, but it makes the 256 x 256 tile
+  // spill, which gains nothing from any of this.
+  __device__ __forceinline__ static void store_slabs(const Args& a, const Unit& u, Acc& acc, char* smem) {
+    constexpr int LPR = Cfg::WTN / 8, RPI8 = 64 / LPR, IT = 32 / RPI8, CH4 = Cfg::WTN / 4, SLAB = 32 * Cfg::WTN * 4;
+    static_assert(LPR >= 4 && LPR <= 8 && Cfg::NW * SLAB <= Cfg::STAGES * Cfg::STAGE_BYTES, "slab");
+    const int w = wave_id(), l = lane_id();
+    const int wm = w / Cfg::WAVES_N, wn = w % Cfg::WAVES_N;
+    char* st = smem + w * SLAB;
+    const bool add = a.c_type >= 0 && a.beta != 0.f, c32 = a.c_type == DT_F32;
+    const int col = l % LPR * 8, n = u.n0 + wn * Cfg::WTN + col, left = a.N - n;
+#pragma unroll
+    for (int sl = 0; sl < TM; ++sl) {
+      const int64_t m0 = u.m0 + wm * Cfg::WTM + sl * 32;
+      Raw<DT_F32> c[IT];  // (16-bit types: the first half)
+      if (add) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+          const int64_t m = m0 + i * RPI8 + l / LPR;
+          const int have = m < u.m_end ? left : 0;
+          const char* p = (const char*)a.C + (m * a.ldc + n) * (c32 ? 4 : 2);
+          if (c32) {
+            c[i].template load<true>(p, have);
+          } else {
+            Raw<DT_BF16> h;
+            h.template load<true>(p, have);
+            c[i].d[0] = h.d[0];
+          }
+        }
+      }
+      const int at = row_of(0, l);
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          *(f32x4*)(st + at * (Cfg::WTN * 4) + (((col_of(tn, g, l) / 4) ^ swz<CH4>(at)) << 4)) =
+              f32x4{value(acc, tn, sl, 4 * g), value(acc, tn, sl, 4 * g + 1), value(acc, tn, sl, 4 * g + 2), value(acc, tn, sl, 4 * g + 3)};
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // this wave's LDS writes are done (lgkmcnt 0)
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        const int row = i * RPI8 + l / LPR;
+        const int64_t m = m0 + row;
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 x = *(const f32x4*)(st + row * (Cfg::WTN * 4) + (((col / 4 + h) ^ swz<CH4>(row)) << 4));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * h + j] = a.alpha * x[j];
+        }
+        if (add) {
+          Raw<DT_BF16> hb;
+          Raw<DT_F16> hf;
+          hb.d[0] = hf.d[0] = c[i].d[0];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = __builtin_fmaf(a.beta, c32 ? c[i].at(j) : a.c_type == DT_BF16 ? hb.at(j) : hf.at(j), v[j]);
+        }
+        const int have = m < u.m_end ? left : 0;
+        char* p = (char*)a.D + (m * a.ldd + n) * (a.d_type == DT_F32 ? 4 : 2);
+        if (a.d_type == DT_F32)
+          store8<DT_F32, false>(p, v, have);
+        else if (a.d_type == DT_BF16)
+          store8<DT_BF16, true>(p, v, have);
+        else
+          store8<DT_F16, true>(p, v, have);
+      }
+    }
+    lds_barrier();  // the next unit's ring; the stores drain behind its loads
   }
 
   // f(m, n, tn, tm, g) for the lane's groups of four columns inside the matrix
