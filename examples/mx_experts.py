@@ -1,5 +1,5 @@
-"""An expert block served in MXFP4: router choice -> gather and quantise -> gate and up products -> SwiGLU and quantise ->
-down products -> weighted sum of each token's experts.
+"""An expert block served in MXFP4: router choice -> choices sorted by expert -> gather and quantise -> gate and up products ->
+SwiGLU and quantise -> down products -> weighted sum of each token's experts.
 
     python examples/mx_experts.py [--tokens T] [--experts E] [--top-k K] [--hidden H] [--inner I]
 
@@ -64,7 +64,8 @@ class ExpertBlock:
         self.gate_up = torch.empty(rows, 2 * self.inner, device="cuda", dtype=torch.bfloat16)
         self.out = torch.empty(rows, self.hidden, device="cuda", dtype=torch.bfloat16)
         self.op = qg.operation(quant_a=MX, quant_b=MX)
-        self.edges = torch.arange(self.experts + 1, device="cuda")
+        self.offsets = torch.empty(self.experts + 1, device="cuda", dtype=torch.int32)
+        self.rows, self.back = (torch.empty(rows, device="cuda", dtype=torch.int32) for _ in range(2))
 
     def product(self, a, w, d, offsets):
         (ad, ud), (bd, vd) = a.grouped(self.experts, offsets), w.weights()
@@ -73,16 +74,17 @@ class ExpertBlock:
 
     def __call__(self, x, ids, weights):
         """x: tokens x H bfloat16; ids, weights: tokens x top_k (each token's experts and their shares)."""
-        owner, order = ids.flatten().sort(stable=True)
-        rows = (order // self.top_k).int()
-        offsets = torch.searchsorted(owner, self.edges).int()
-        self.x.fill(self.engine, x, rows=rows)
-        self.product(self.x, self.w1, self.gate_up, offsets)
+        ids, weights = ids.int().contiguous(), weights.float().contiguous()
+        self.engine.group_rows(self.experts, ids, qg.layout("i32", self.tokens, self.top_k), self.offsets, self.rows, self.back,
+                               self.space.desc)
+        self.x.fill(self.engine, x, rows=self.rows)
+        self.product(self.x, self.w1, self.gate_up, self.offsets)
         self.h.fill(self.engine, self.gate_up, act=qg.MX_SWIGLU)
-        self.product(self.h, self.w2, self.out, offsets)
-        back = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device="cuda"))
-        y = self.out[back].view(self.tokens, self.top_k, self.hidden).float()
-        return (y * weights[..., None].float()).sum(1)
+        self.product(self.h, self.w2, self.out, self.offsets)
+        y = torch.empty(self.tokens, self.hidden, device="cuda")
+        self.engine.combine(self.out, qg.layout("bf16", *self.out.shape), self.back, weights, qg.layout("f32", self.tokens, self.top_k),
+                            y, qg.layout("f32", self.tokens, self.hidden))
+        return y
 
 
 def main():
@@ -99,7 +101,10 @@ def main():
     w2 = torch.randn(a.experts, a.hidden, a.inner, device="cuda", dtype=torch.bfloat16) * 0.02
     block = ExpertBlock(engine, w1, w2, a.tokens, a.top_k)
     x = torch.randn(a.tokens, a.hidden, device="cuda", dtype=torch.bfloat16)
-    share, ids = torch.randn(a.tokens, a.experts, device="cuda").softmax(-1).topk(a.top_k, -1)
+    logits = torch.randn(a.tokens, -(-a.experts // 4) * 4, device="cuda")
+    ids, share = torch.empty(a.tokens, a.top_k, device="cuda", dtype=torch.int32), torch.empty(a.tokens, a.top_k, device="cuda")
+    engine.route(qg.routing(qg.ROUTE_SOFTMAX, a.top_k, renormalize=True), logits, qg.layout("f32", a.tokens, a.experts, ld=logits.shape[1]),
+                 None, ids, qg.layout("i32", a.tokens, a.top_k), share, qg.layout("f32", a.tokens, a.top_k))
     for _ in range(3):
         y = block(x, ids, share)
     begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)

@@ -564,16 +564,27 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a) {
 
 template <int DT, int NV>
 hipError_t route_nv(const RouteArgs& a, hipStream_t s) {
-  const int64_t blocks = std::min<int64_t>((a.T + 3) / 4, 1 << 20);
+  const int64_t blocks = std::min<int64_t>(((int64_t)a.T + 3) / 4, 1 << 20);
   hipLaunchKernelGGL((route_kernel<DT, NV>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT, int NV>
-hipError_t route_rows(RouteArgs a, hipStream_t s) {
-  a.shift -= 2;  // a group's lanes among 16
-  hipLaunchKernelGGL((route_rows_kernel<DT, NV>), dim3((unsigned)((a.T + 15) / 16)), dim3(256), 0, s, a);
-  return hipGetLastError();
+hipError_t route_rows(const RouteArgs& a, hipStream_t s) {
+  // a dispatch counts its threads in 32 bits: tokens go out in parts of fewer
+  constexpr int64_t kMost = int64_t(1) << 27;
+  for (int64_t t = 0; t < a.T; t += kMost) {
+    RouteArgs p = a;
+    p.T = (int32_t)std::min<int64_t>(kMost, a.T - t);
+    p.X = (const char*)a.X + t * a.ldx * (DT == DT_F32 ? 4 : 2);
+    p.ids = a.ids + t * a.ldi;
+    p.W = a.W + t * a.ldw;
+    p.shift = (int8_t)(a.shift - 2);  // a group's lanes among 16
+    hipLaunchKernelGGL((route_rows_kernel<DT, NV>), dim3((unsigned)(((int64_t)p.T + 15) / 16)), dim3(256), 0, s, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int DT>

@@ -216,3 +216,21 @@ def test_no_tokens(g):
     x = torch.zeros(1, 8, device="cuda")
     g.route(qg.routing(top_k=2), x, qg.layout("f32", 0, 8), None, ids, qg.layout("i32", 0, 2), w, qg.layout("f32", 0, 2))
     assert (ids == 9).all() and (w == 9).all()
+
+
+def test_tokens_past_2_to_the_32_threads(g):
+    """2^28 tokens take 2^32 threads at 16 each: they go out in parts, and the last ones are written too."""
+    t = (1 << 28) + 5
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of free device memory")
+    x = torch.zeros(t, 8, device="cuda", dtype=torch.bfloat16)
+    x[:, 1] = 1
+    x[-1, 0] = 2
+    x[(1 << 27) - 1, 2], x[1 << 27, 3] = 3, 3
+    ids = torch.full((t, 1), -7, dtype=torch.int32, device="cuda")
+    w = torch.empty(t, 1, device="cuda")
+    g.route(qg.routing(qg.ROUTE_SOFTMAX, 1, renormalize=True), x, qg.layout("bf16", t, 5, ld=8), None, ids, qg.layout("i32", t, 1), w,
+            qg.layout("f32", t, 1))
+    ids = ids.flatten()
+    assert ids[-1] == 0 and ids[(1 << 27) - 1] == 2 and ids[1 << 27] == 3
+    assert int((ids == 1).sum()) == t - 3 and bool((w == 1).all())
