@@ -36,7 +36,6 @@ namespace {
 const char* kVersion = "qgemm 0.1.0";
 const size_t kBarriersSize = size_t(1) << 20;
 const size_t kPartialsSize = size_t(32) << 20;
-const double kMemorySideCache = 256.0 * (1 << 20);
 const int kTuningSeq[] = {1,   2,   4,   8,    16,   24,   32,   48,   64,   96,   128,  192,
                           256, 384, 512, 768, 1024, 1536, 2048, 3072, 4096, 6144, 8192};
 
@@ -539,6 +538,12 @@ int find_kernel(const char* name) {
   return -1;
 }
 
+// Whether the operands pass the 256 MB of the memory-side cache.
+bool past_cache(const Problem& p) {
+  const double a = (double)p.M * p.lda * (p.batched ? p.E : 1), b = (double)p.N * p.ldb * (p.E > 0 && p.b_batch ? p.E : 1);
+  return a + b > 256.0 * (1 << 20);
+}
+
 // Builds the launch for a choice; checks the workspace.
 int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_workspace* ws, Plan& pl) {
   if (c.kernel < 0 || c.kernel >= kNumKernels) return QG_ERR_NO_KERNEL;
@@ -661,10 +666,7 @@ int make_plan(const qg_handle* h, const Problem& p, const Choice& c, const qg_wo
     a.counters = (int32_t*)ws->barriers;
   }
   a.grid = pl.grid;
-  if (p.ta == QG_I8) {
-    const double a_bytes = (double)p.M * p.lda * (p.batched ? p.E : 1), b_bytes = (double)p.N * p.ldb * (p.E > 0 && p.b_batch ? p.E : 1);
-    a.ahead = a_bytes + b_bytes > kMemorySideCache;
-  }
+  a.ahead = p.ta == QG_I8 && past_cache(p);
   return QG_OK;
 }
 
@@ -762,20 +764,24 @@ Choice mx_heuristic(const qg_handle* h, const Problem& p, const qg_workspace* ws
 }
 
 // int8 over experts. Up to 16 rows on average stream B through small workgroups that share A (three per CU), more take the
-// tile with the least estimated time: a CU that has n tiles takes n (fixed + step per 128 of K). Measured, us, skinny
-// 16 x 64 / tiles of 32 x 128 / 128 x 128 / 256 x 256:
-//   64 experts, N 2048, K 7168:    128 rows 153 / 162 / 200 / 219    1024 rows  179 / 189 / 189 / 241
-//                                 4096 rows 346 / 297 / 240 / 255    8192 rows  557 / 495 / 289 / 342
-//                                16384 rows   - / 939 / 456 / 368
-//   256 experts, 4096 rows, N 1536, K 2048    169 / 176 / 208 / 225   8 experts, 200 rows, N, K 4096   30 / 27 / 30 / 47
-//   24 experts, 1501 rows, N 1000, K 2075      30 / 29 / 24 / 38      128 experts, 95 rows, N 5120, K 468   48 / 97 / 142 / 112
-//   8 experts, 1000 rows, N 14336, K 4096     315 / 275 / 156 / 161   32 experts, 40000 rows, N 1408, K 2048   - / 554 / 271 / 160
+// tile with the least estimated time: a CU that has n tiles takes n (fixed + step per 128 of K), the step of the 256 x 256
+// tile, whose ring is two deep, being longer where its operands come from HBM. Measured, us, skinny 16 x 64 / tiles of
+// 32 x 128 / 128 x 128 / 128 x 256 / 256 x 256:
+//   64 experts, N 2048, K 7168:    128 rows 153 / 162 / 200 /  - / 219    1024 rows  179 / 189 / 189 / 179 / 241
+//                                 4096 rows 346 / 297 / 232 / 227 / 255   8192 rows  557 / 495 / 297 / 240 / 328
+//                                16384 rows   - / 939 / 449 / 353 / 371  65536 rows    - / 3300 / 1516 / 1148 / 1006
+//   256 experts, 4096 rows, N 1536, K 2048    169 / 176 / 199 / 171 / 224
+//   24 experts, 1501 rows, N 1000, K 2075      30 / 29 / 24 / 28 / 38
+//   8 experts, 200 rows, N, K 4096             30 / 27 / 29 / 32 / 47
+//   128 experts, 95 rows, N 5120, K 468        48 / 97 / 142 / - / 112
+//   8 experts, 1000 rows, N 14336, K 4096     315 / 275 / 157 / 134 / 159
+//   32 experts, 40000 rows, N 1408, K 2048      - / 554 / 277 / 192 / 161
 int i8_grouped(const qg_handle* h, const Problem& p) {
   if (p.M <= (int64_t)16 * p.E) return kernel_by_shape(p, 16, 64);
-  static const struct {
+  const struct {
     int bm, bn;
     double fixed, step;
-  } kTiles[] = {{32, 128, 2.5, 0.35}, {128, 128, 4, 0.62}, {256, 256, 9, 1.9}};
+  } kTiles[] = {{32, 128, 2.5, 0.35}, {128, 128, 4, 0.62}, {128, 256, 5, 1.1}, {256, 256, 9, past_cache(p) ? 1.9 : 1.35}};
   const double live = (double)std::min<int64_t>(p.E, p.M);
   int kernel = -1;
   double best = 0;
