@@ -7,11 +7,14 @@
 // where a wave's entries of an expert go. Within 64 entries, the lanes that hold
 // the same expert find each other by a ballot per bit of the expert's number.
 // No atomic's order is visible in the results. Bound by latency: 4 bytes in
-// and 8 out per entry are nothing beside two passes of dependent LDS accesses.
+// and 8 out per entry are nothing beside two passes of dependent LDS accesses. Measured: 128 choices over 64
+// experts 4.0 us, 524288 over 256 15.5 us (two launches; 18.5 with 128 ranges; 96 with the table of counts summed by a
+// thread per two experts, a load at a time).
 //
 // Combination: y[t] = sum_k w[t, k] r[back[t, k]] + beta c[t], k in order, in
 // fp32, rounded once. A lane takes 8 columns of one token and has eight of
-// its rows' loads in flight. Bound by memory: each result is read once.
+// its rows' loads in flight. Bound by memory: each result is read once (8192 tokens of 8 x 7168, bf16, plus a
+// shared expert's: 230 us, 5.1 TB/s).
 #include "qg_experts.hpp"
 
 #include <algorithm>

@@ -3,20 +3,25 @@
 // A row of y (the row itself, or silu(gate) * up) with largest magnitude amax
 // has the scale s = fp32(amax / 127) and the codes rne(y / s), both as 64-bit
 // arithmetic gives them: a row's maximum has to be known before its first
-// code, so a row is read once into registers (up to 16384 elements, 65536 with
-// four times the waves) and its codes leave from there; longer ones are read twice.
+// code, so a row is read once into registers (up to 65536 elements: 1024 lanes
+// of 64) and its codes leave from there.
 //
 // fp32 decides what it can. With t = v * (1 / s), where v is the fp32 value,
 // the code is rint(t) unless t is within its error of a half: then that
-// element alone is done again in 64 bits, from memory (the caches have it).
-// The error of t: identity 2^-23 t. SwiGLU: v = (g u) rcp(1 + exp2(-g log2 e)):
-// the argument of exp2 is off by 2.25 * 2^-24 of itself (the constant's rounding, the
-// product's), so e by |g| 2.25 * 2^-24 of itself, the other steps by 8 * 2^-24 (exp2 and rcp
-// one step each, the sum, three products): within 2^-19 for g >= -8 and 2^-17 for
-// g >= -32 (below that exp2 may overflow: always in 64 bits). The maximum of a gated row is taken in 64 bits
-// too, over the elements whose v is within 2^-16 of the largest v. Rows whose
-// largest v is not finite, or so small that v or the scale may have lost bits
-// (below 2^-60), go through 64 bits as a whole.
+// element alone is done again in 64 bits, from memory (the caches have it), and
+// stored over the first code. The error of t: identity 2^-23 t. SwiGLU: v = (g u) rcp(1 +
+// exp2(-g log2 e)): the argument of exp2 is off by 1.25 * 2^-24 of itself (the product's rounding,
+// the constant's), so e by |g| 1.25 * 2^-24 of itself, the other steps by 8 * 2^-24 (exp2 and rcp
+// 2^-23 each, the sum, three products), 1 / s and its product by 2^-23: within 2^-19 for
+// g >= -8 and 2^-17 for g >= -32 (below that exp2 may overflow: always in 64 bits). The maximum of a
+// gated row is taken in 64 bits too, over the elements whose v is within 2^-16 of the largest v. Rows whose
+// largest v is not finite, or so small that v or the scale may have lost bits (below 2^-60), go
+// through 64 bits as a whole.
+//
+// Bound by memory. Measured, bf16: 8192 x 14336 gated 124 us (587 MB, 4.7 TB/s; a copy of 1 GiB reaches 5.15), 8192 x
+// 7168 gated 56 (5.2), 8192 x 14336 63 (5.6), 4096 rows gathered to 32768 x 7168 116 (each row read eight times, 705 MB
+// through the memory-side cache; its own 294 MB would take 57), the same codes back to values 98 (7.2 TB/s: the codes come from the
+// memory-side cache), one row of 4096 2.7 us and 2.0 back.
 #include "qg_i8_quant.hpp"
 
 #include <algorithm>
@@ -55,7 +60,7 @@ __device__ __forceinline__ double lanes_max(double x) {
 }
 
 // L lanes (a part of a wave, or whole waves: the workgroup) take one row,
-// U units of 8 elements each.
+// U units of 8 elements each. (512 gated lanes: registers for two workgroups per CU, which load in turn.)
 template <int DT, bool GATED, int L, int U>
 __global__ __launch_bounds__(L < 256 ? 256 : L, GATED && L == 512 ? 4 : 1) void i8_quantize_kernel(const I8QuantArgs a) {
   constexpr int NT = L < 256 ? 256 : L, RPB = NT / L, LW = L < 64 ? L : 64, NW = L / 64;
@@ -158,15 +163,16 @@ __global__ __launch_bounds__(L < 256 ? 256 : L, GATED && L == 512 ? 4 : 1) void 
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int k = (i * L + l) * 8, n = live ? a.K - k : 0;
-    // a code is the low byte of t + 1.5 * 2^23, which rounds t to an integer (ties to even)
+    // a code is the low byte of v / s + 1.5 * 2^23, which rounds to an integer (ties to even)
     constexpr float kRound = 12582912.f;
     const float off = !GATED ? 0x1p-22f : low[GATED ? i : 0] < -8.f ? 0x1p-17f : 0x1p-19f;
     uint32_t c[8], q[2];
     float worst = 0.f;
     const auto doubt = [&](int j, uint32_t& code) {
-      const float t = val(i, j) * inv, r = t + kRound;
+      // (fmas spelled out: both evaluations of an element are the same)
+      const float x = val(i, j), r = __builtin_fmaf(x, inv, kRound);
       code = __builtin_bit_cast(uint32_t, r);
-      return __builtin_fmaf(fabsf(t), off, fabsf(t - (r - kRound)));
+      return __builtin_fmaf(fabsf(x * inv), off, fabsf(__builtin_fmaf(x, inv, kRound - r)));
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) worst = fmaxf(worst, doubt(j, c[j]));
@@ -260,9 +266,9 @@ hipError_t quantize_lu(const I8QuantArgs& a, hipStream_t s) {
 }
 
 // Lanes per row and units per lane, so that a row just fits: a lane of one wave has up to four units, of several up to four
-// too, of 1024 lanes eight. bf16, 8192 rows gated: K 14336 139 us with 512 lanes of four units (two such workgroups per
-// CU), 168 with 256 of eight, 193 with 1024 of two; K 7168 58 with 256 of four. 32768 rows gathered, K 7168: 107 with 256 of
-// four, 133 with one wave of 16, 112 with two of eight; 125 with the next row's loads ahead of this one's work.
+// too, of 1024 lanes eight. bf16, 8192 rows gated, K 14336: 124 us with 512 lanes of four units (two such workgroups per CU;
+// 176 with the registers that one takes), 168 with 256 of eight, 193 with 1024 of two. 32768 rows gathered, K 7168: 107 to 116 with
+// 256 of four, 133 with one wave of 16, 112 with two of eight; 125 with the next row's loads ahead of this one's work.
 template <int DT, bool GATED>
 hipError_t quantize_t(const I8QuantArgs& a, hipStream_t s) {
   if (a.cpr <= 8) return quantize_lu<DT, GATED, 8, 1>(a, s);
