@@ -339,8 +339,9 @@ int qg_route(qg_handle* h, const qg_routing* routing, const void* X, const qg_la
  *   offsets  DEVICE, experts + 1: the `offsets` of a grouped qg_run over T * K rows.
  *   rows     DEVICE, T * K: the token of each sorted row, the `rows` of a quantiser; -1 behind offsets[experts].
  *   back     DEVICE, T * K: the sorted row of each choice, -1 for nobody's; qg_combine's `back`.
- * experts is at most 1023, T * K at most 2^30. `ws` may be NULL for up to 8192 choices; beyond, 1024 bytes of its
- * partials per expert are used. Asynchronous on `stream`, allocates nothing. */
+ * experts is at most 1023, T * K at most 2^30. `ws` may be NULL for up to 8192 choices; where it is given, 1024 bytes of its
+ * partials per expert may be used, so calls that run at the same time need workspaces of their own, as runs do.
+ * Asynchronous on `stream`, allocates nothing. */
 int qg_group_rows(qg_handle* h, int experts, const int32_t* ids, const qg_layout* Idesc, int32_t* offsets, int32_t* rows,
                   int32_t* back, const qg_workspace* ws, hipStream_t stream);
 
