@@ -15,7 +15,9 @@
 // Keys are those of 64-bit arithmetic: fp32 decides where two neighbours in the
 // order (or the groups on both sides of the cut) are further apart than the
 // errors of their keys, or have the same key (equal logit, equal bias); a
-// token where they are not is done again in 64 bits, by its wave. Errors of an
+// token where they are not is done again in 64 bits, by its wave. At the cut
+// the last one chosen has to stand above everything that is left out, whose
+// errors may be larger than that of the first of them. Errors of an
 // fp32 score, relative, in 2^-23, exp2 and rcp being good to 1 each: e^x is off
 // by 0.61 |x| (the product's rounding, the constant's) + 1. Sigmoid: (1 - s) of that (what
 // e does to 1 / (1 + e)), 0.5 for the sum, 1 for rcp: at most 4 + |x| (1 - s). Softmax: its
@@ -236,6 +238,11 @@ struct Scores {
     const float rel = sigmoid ? 4.f + fminf(fabsf(x), 128.f) * (1.f - s) : 16.f + (x == m ? 0.f : 1.5f * fminf(m - x, 128.f));
     return (s * rel + fabsf(k)) * 0x1p-23f + 0x1p-120f;
   }
+  // The same for every key of up to k, whatever its score: s rel is at most 4.3 for a sigmoid and 16 of the largest
+  // score for a softmax, and k + |k| 2^-23 grows with k.
+  __device__ __forceinline__ float error_up_to(float k) const {
+    return ((sigmoid ? 5.f : 17.f * total) + fabsf(k)) * 0x1p-23f + 0x1p-120f;
+  }
 };
 // How far the standings of two groups may be off together. With a bias: two scores each (at most 5, or 16, times
 // 2^-23), and the roundings of four keys of up to `most` and two sums. Without: scores of up to e^-88 (smaller
@@ -324,9 +331,11 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs a) {
       mine = choose(key, e0, a.bias ? a.K + 1 : a.K, found);
       if (mine >= 0) l = logit<DT>(a, t, mine);
       if (a.bias) {
-        // every key against the next one: too near to call, and not the same expert twice?
+        // every key against the next one (the last one chosen: against all that are left out): too near to call, and not
+        // the same expert twice?
         const float b = mine >= 0 ? a.bias[mine] : 0.f, s = sc.raw(l) * sc.total, k = s + b, err = sc.error(l, s, k);
-        const float ln = __shfl_down(l, 1, 64), bn = __shfl_down(b, 1, 64), kn = __shfl_down(k, 1, 64), en = __shfl_down(err, 1, 64);
+        const float ln = __shfl_down(l, 1, 64), bn = __shfl_down(b, 1, 64), kn = __shfl_down(k, 1, 64);
+        const float ek = __shfl_down(err, 1, 64), en = lane == a.K - 1 ? sc.error_up_to(kn) : ek;
         redo = __any(lane + 1 < found && !(k - kn > err + en) && !(l == ln && b == bn));
       }
     }
@@ -524,7 +533,8 @@ __global__ __launch_bounds__(256) void route_rows_kernel(const RouteArgs a) {
   float x = mine >= 0 ? logit<DT>(a, t, mine) : 0.f;
   if (a.bias) {
     const float b = mine >= 0 ? a.bias[mine] : 0.f, s = sc.raw(x) * sc.total, k = s + b, err = sc.error(x, s, k);
-    const float xn = __shfl_down(x, 1, 64), bn = __shfl_down(b, 1, 64), kn = __shfl_down(k, 1, 64), en = __shfl_down(err, 1, 64);
+    const float xn = __shfl_down(x, 1, 64), bn = __shfl_down(b, 1, 64), kn = __shfl_down(k, 1, 64);
+    const float ek = __shfl_down(err, 1, 64), en = l == a.K - 1 ? sc.error_up_to(kn) : ek;
     unsure |= l + 1 < found && !(k - kn > err + en) && !(x == xn && b == bn);
   }
   uint64_t redo = __ballot(unsure);
