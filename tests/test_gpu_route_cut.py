@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import quantized_gemm_bf16_amd as qg
-from tests.test_gpu_route import MANY, check
+from tests.test_gpu_route import MANY, check, logits
 
 pytestmark = pytest.mark.gpu
 FEW = 300  # a token per wave
@@ -60,3 +60,47 @@ def test_example(g):
 def test_errors_of_different_size(g, t, sigmoid, top_k, gap):
     x, bias = mixed(t, top_k, gap, sigmoid, top_k)
     check(g, x, "f32", top_k, bias=bias, sigmoid=sigmoid)
+
+
+@pytest.mark.parametrize("t", [FEW, MANY])
+@pytest.mark.parametrize("bias", [0.0, 0.25])
+@pytest.mark.parametrize("top_k", [1, 2, 5, 15])
+def test_equal_experts_on_both_sides_of_the_cut(g, t, bias, top_k):
+    """Scores of a sigmoid that fp32 rounds to 1: top_k + 1 or more equal experts, then better ones of higher index."""
+    r = np.random.default_rng(top_k)
+    x = logits(t, 40, "bf16", top_k)
+    for row in x:
+        at = np.sort(r.permutation(40)[:top_k + 1 + r.integers(1, 9)])
+        row[at] = 20.0
+        row[at[top_k + 1:]] = r.integers(20, 23, len(at) - top_k - 1)
+    x[0] = 0.0
+    x[0, [3, 8, 30]] = 20.0, 20.0, 21.0
+    check(g, x, "f32", top_k, bias=np.full(40, bias), sigmoid=True)
+    check(g, x, "bf16", top_k, bias=np.full(40, bias), sigmoid=True, renormalize=True)
+    check(g, x, "f32", top_k, bias=np.full(40, bias), sigmoid=True, groups=5, top_groups=4, group_best=1)
+
+
+@pytest.mark.parametrize("t", [FEW, MANY])
+@pytest.mark.parametrize("top_k", [2, 3, 5, 15])
+def test_equal_small_scores_of_a_softmax(g, t, top_k):
+    """One logit takes the softmax; the others' scores vanish beside a bias that all have, the equal ones' at the cut too."""
+    r = np.random.default_rng(top_k)
+    x = np.full((t, 40), -9.0)
+    for row in x:
+        at = np.sort(r.permutation(40)[:top_k + 1 + r.integers(1, 9)])
+        row[at[top_k:]] = r.integers(-9, -6, len(at) - top_k)
+        row[at[0]] = 30.0
+    check(g, x, "f32", top_k, bias=np.full(40, 0.25))
+    check(g, x, "bf16", top_k, bias=np.full(40, 0.25), renormalize=True)
+
+
+@pytest.mark.parametrize("t", [FEW, MANY])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_equal_pairs_at_the_cut(g, t, sigmoid):
+    """Whole numbers and halves: pairs at the cut with nothing near them, with a third equal one, and with nothing behind them."""
+    r = np.random.default_rng(3)
+    x = r.integers(-8, 9, (t, 24)) * 0.5
+    x[::3, 9:] = -np.inf
+    for k in (1, 4, 8, 9, 15):
+        check(g, x, "f32", k, bias=np.zeros(24), sigmoid=sigmoid)
+        check(g, x, "f32", k, bias=f32(np.arange(24) % 3 * 0.125), sigmoid=sigmoid)
