@@ -130,13 +130,14 @@ struct Plan {
 namespace {
 
 // Memo of resolved DEFAULT-policy choices, keyed by everything the cache
-// lookup and the heuristic read (exact M, problem key fields, workspace
-// sizes). It turns a repeated call into one hash lookup instead of
-// formatting text keys and probing the tuning-sequence buckets; any change to
-// the cache (measure, import) clears it.
+// lookup and the heuristic read (exact M, problem key fields, whether the
+// operands at their pitches pass the memory-side cache, workspace sizes). It
+// turns a repeated call into one hash lookup instead of formatting text keys
+// and probing the tuning-sequence buckets; any change to the cache (measure,
+// import) clears it.
 struct MemoKey {
   int64_t M, N, K;
-  int32_t ta, tb, tc, td, qa, qb, E, batched, epi, pad;
+  int32_t ta, tb, tc, td, qa, qb, E, batched, epi, past_cache;
   uint64_t ws_partials, ws_barriers;
   bool operator==(const MemoKey& o) const { return memcmp(this, &o, sizeof o) == 0; }
 };
@@ -1027,6 +1028,7 @@ MemoKey memo_key(const Problem& p, const qg_workspace* ws) {
   k.M = p.M, k.N = p.N, k.K = p.K;
   k.ta = p.ta, k.tb = p.tb, k.tc = p.tc, k.td = p.td, k.qa = p.qa, k.qb = p.qb;
   k.E = p.E, k.batched = p.batched, k.epi = p.epi;
+  k.past_cache = p.E > 0 && p.ta == QG_I8 && past_cache(p);  // (i8_grouped)
   const bool ws_ok = ws && ws->partials && ws->barriers;
   k.ws_partials = ws_ok ? ws->partials_size : 0;
   k.ws_barriers = ws_ok ? ws->barriers_size : 0;
