@@ -214,7 +214,7 @@ def routing(score=ROUTE_SOFTMAX, top_k=1, groups=1, top_groups=1, group_best=1, 
 
 def _ptr(t):
     """Device address of a tensor; a raw address or None as it is."""
-    if t is None or t.__class__ is int:
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -222,7 +222,7 @@ def _ptr(t):
 # What a call without a layout for an operand reads has to be a contiguous tensor of the type, of `n` elements at least; one
 # with a layout has to be of the type (None and raw addresses are the caller's word).
 def _bad_table(t, dtype, n=0):
-    if t is None or t.__class__ is int:
+    if t is None or isinstance(t, int):
         return OK
     if t.dtype is not dtype:
         return ERR_UNSUPPORTED
@@ -230,7 +230,7 @@ def _bad_table(t, dtype, n=0):
 
 
 def _bad_type(t, dtype):
-    return OK if t is None or t.__class__ is int or t.dtype is dtype else ERR_UNSUPPORTED
+    return OK if t is None or isinstance(t, int) or t.dtype is dtype else ERR_UNSUPPORTED
 
 
 def _check(st, what):
