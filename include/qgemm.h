@@ -349,7 +349,7 @@ int qg_group_rows(qg_handle* h, int experts, const int32_t* ids, const qg_layout
  * what a shared expert (or the residual) gave. Sums are fp32, k in order, rounded once (RNE) to Y's type.
  *   R     f32 | bf16 | fp16, N x H; back: DEVICE, T x K int32, contiguous; an entry outside [0, N) adds nothing.
  *   W     QG_F32, T x K; C (read only when beta != 0) and Y f32 | bf16 | fp16, T x H, rows at multiples of 16 bytes.
- *         Y may be C. Asynchronous on `stream`, allocates nothing. */
+ *         Y may be C, of one type and pitch. Asynchronous on `stream`, allocates nothing. */
 int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_t* back, const float* W, const qg_layout* Wdesc,
                float beta, const void* C, const qg_layout* Cdesc, void* Y, const qg_layout* Ydesc, hipStream_t stream);
 

@@ -1321,6 +1321,8 @@ int qg_combine(qg_handle* h, const void* R, const qg_layout* Rdesc, const int32_
     a.c_type = Cdesc->type;
   }
   if (T == 0 || H == 0) return QG_OK;
+  // in place, each lane's eight columns have to lie where it reads them
+  if (a.C && a.C == Y && (a.c_type != Ydesc->type || (T > 1 && Cdesc->ld != Ydesc->ld))) return QG_ERR_INVALID_ARG;
   a.R = R;
   a.back = back;
   a.W = W;
