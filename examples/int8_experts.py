@@ -66,9 +66,9 @@ class ExpertBlock:
         self.engine.run(self.op, 1.0, a.q, ad, a.s, ud, w.q, bd, w.s, vd, 0.0, None, None, d, dd, self.space.desc)
 
     def __call__(self, x):
-        """x: tokens x H bfloat16; returns x plus its experts' weighted sum."""
+        """x: tokens x H bfloat16, rows at any pitch of 16 bytes; returns x plus its experts' weighted sum."""
         g, t = self.engine, self.tokens
-        xd, ld = qg.layout("bf16", t, self.hidden), qg.layout("f32", t, self.experts)
+        xd, yd, ld = qg.layout("bf16", t, self.hidden, ld=x.stride(0)), qg.layout("bf16", t, self.hidden), qg.layout("f32", t, self.experts)
         kd, wd = qg.layout("i32", t, self.top_k), qg.layout("f32", t, self.top_k)
         g.run(qg.operation(), 1.0, x, xd, None, None, self.router, qg.layout("bf16", self.experts, self.hidden), None, None,
               0.0, None, None, self.logits, ld, self.space.desc)
@@ -78,8 +78,8 @@ class ExpertBlock:
         self.product(self.x, self.w1, self.gate_up)
         self.h.fill(g, self.gate_up, act=qg.MX_SWIGLU)
         self.product(self.h, self.w2, self.out)
-        y = torch.empty_like(x)
-        g.combine(self.out, qg.layout("bf16", *self.out.shape), self.back, self.weights, wd, y, xd, beta=1.0, C=x, Cd=xd)
+        y = torch.empty(t, self.hidden, device="cuda", dtype=torch.bfloat16)
+        g.combine(self.out, qg.layout("bf16", *self.out.shape), self.back, self.weights, wd, y, yd, beta=1.0, C=x, Cd=xd)
         return y
 
 
