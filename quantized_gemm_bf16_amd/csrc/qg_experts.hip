@@ -8,8 +8,8 @@
 // the same expert find each other by a ballot per bit of the expert's number.
 // No atomic's order is visible in the results. Bound by latency: 4 bytes in
 // and 8 out per entry are nothing beside two passes of dependent LDS accesses. Measured: 128 choices over 64
-// experts 4.0 us, 524288 over 256 15.5 us (two launches; 18.5 with 128 ranges; 96 with the table of counts summed by a
-// thread per two experts, a load at a time).
+// experts 3.6 us, 524288 over 256 15.5 us (two launches, 4.7 and 12.4 in a trace, where each takes longer; 18.5 with 128
+// ranges; 96 with the table of counts summed by a thread per two experts, a load at a time).
 //
 // Combination: y[t] = sum_k w[t, k] r[back[t, k]] + beta c[t], k in order, in
 // fp32, rounded once. A lane takes 8 columns of one token and has eight of

@@ -18,10 +18,10 @@
 // largest v is not finite, or so small that v or the scale may have lost bits (below 2^-60), go
 // through 64 bits as a whole.
 //
-// Bound by memory. Measured, bf16: 8192 x 14336 gated 124 us (587 MB, 4.7 TB/s; a copy of 1 GiB reaches 5.15), 8192 x
-// 7168 gated 56 (5.2), 8192 x 14336 63 (5.6), 4096 rows gathered to 32768 x 7168 116 (each row read eight times, 705 MB
-// through the memory-side cache; its own 294 MB would take 57), the same codes back to values 98 (7.2 TB/s: the codes come from the
-// memory-side cache), one row of 4096 2.7 us and 2.0 back.
+// Bound by memory. Measured, bf16: 8192 x 14336 gated 124 to 128 us (587 MB, 4.7 TB/s; a copy of 1 GiB reaches 5.15), 8192 x
+// 7168 gated 56 (5.2), 8192 x 14336 63 (5.6), 4096 rows gathered to 32768 x 7168 97 to 102 (each row read eight times, 705 MB
+// through the memory-side cache; its own 294 MB would take 63), the same codes back to values 117 to 125 (5.7 to 6.0 TB/s;
+// the 470 MB written alone would take 107 at the rate that a copy's writes reach), one row of 4096 2.2 to 2.6 us and 1.7 to 1.9 back.
 #include "qg_i8_quant.hpp"
 
 #include <algorithm>
@@ -267,8 +267,8 @@ hipError_t quantize_lu(const I8QuantArgs& a, hipStream_t s) {
 
 // Lanes per row and units per lane, so that a row just fits: a lane of one wave has up to four units, of several up to four
 // too, of 1024 lanes eight. bf16, 8192 rows gated, K 14336: 124 us with 512 lanes of four units (two such workgroups per CU;
-// 176 with the registers that one takes), 168 with 256 of eight, 193 with 1024 of two. 32768 rows gathered, K 7168: 107 to 116 with
-// 256 of four, 133 with one wave of 16, 112 with two of eight; 125 with the next row's loads ahead of this one's work.
+// 176 with the registers that one takes), 168 with 256 of eight, 193 with 1024 of two. 32768 rows gathered, K 7168, one after the
+// other: 107 to 116 with 256 of four, 133 with one wave of 16, 112 with two of eight; 125 with the next row's loads ahead of this one's work.
 template <int DT, bool GATED>
 hipError_t quantize_t(const I8QuantArgs& a, hipStream_t s) {
   if (a.cpr <= 8) return quantize_lu<DT, GATED, 8, 1>(a, s);

@@ -9,8 +9,9 @@
 // index order, a group is an aligned run of lanes, and the lowest lane of a
 // ballot is the lowest index. A round of the choice is a maximum of the
 // keys as ordered integers over the token's lanes (DPP), a ballot for its place, and the removal of that key.
-// Bound by instruction issue: 16384 tokens over 256 experts read 17 MB (3.5 us), and take 8.6 us where the logits
-// alone decide, 14.6 with a bias, 19 with groups too, tokens in doubt included (about 5 us for each, among others).
+// 16384 tokens over 256 experts read 17 MB (2.7 us), and take 8.3 us where the logits alone decide, 14 to 16 with a
+// bias, 18 to 20 with groups too, tokens in doubt included (about 5 us for each, among others). Of the 18 us each SIMD's
+// vector instructions (5500 of four cycles) take half; the rest is latency that its four waves do not cover.
 //
 // Keys are those of 64-bit arithmetic: fp32 decides where two neighbours in the
 // order (or the groups on both sides of the cut) are further apart than the
